@@ -339,7 +339,7 @@ def run(state):
         if c["cache"] == "e4m3":
             return dict(out, k=state["k"], v=state["v"])
         k, v = d.kv_read(cache, state["table"], state["past"], state["cu"], tokens=qkv.shape[0],
-                         dtype=qkv.dtype)
+                         max_tokens=state["max_new"], dtype=qkv.dtype)
         return dict(out, k=k, v=v)
     return {"w4": _w4_plain, "append": _append_plain, "attend": _attend_plain}[c["op"]](state)
 
