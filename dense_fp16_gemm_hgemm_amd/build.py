@@ -8,7 +8,8 @@ instructions are disabled for all device code.
 It also builds ``dense_fp16_gemm_hgemm_amd/libmi_overlap.so`` (the load/compute
 overlap micro-benchmark, ``overlap/overlap.hip``),
 ``dense_fp16_gemm_hgemm_amd/libmi_ceiling.so`` (the MFMA, copy and HBM read
-ceilings, ``ceiling/ceiling.hip``) and, where rocBLAS is
+ceilings, ``ceiling/ceiling.hip``), ``dense_fp16_gemm_hgemm_amd/libmi_decode.so``
+(the decode operators, ``decode/``) and, where rocBLAS is
 installed, ``dense_fp16_gemm_hgemm_amd/mi_hgemm_serve``, the server-mode load
 generator (``serve/serve_bench.cpp``), linked against the library (found beside
 it at run time) and rocBLAS (the vendor backend it compares with).  Without
@@ -34,6 +35,8 @@ OVERLAP_SRC = os.path.join(PKG, "overlap", "overlap.hip")
 OVERLAP_PATH = os.path.join(PKG, "libmi_overlap.so")
 CEILING_SRC = os.path.join(PKG, "ceiling", "ceiling.hip")
 CEILING_PATH = os.path.join(PKG, "libmi_ceiling.so")
+DECODE_SRC = os.path.join(PKG, "decode")
+DECODE_PATH = os.path.join(PKG, "libmi_decode.so")
 SERVE_SRC = os.path.join(PKG, "serve", "serve_bench.cpp")
 SERVE_PATH = os.path.join(PKG, "mi_hgemm_serve")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -52,13 +55,13 @@ DEVICE = ["--offload-arch=" + ARCH,
           "-Wno-unused-command-line-argument"]
 
 
-def _compile_cmds():
+def _compile_cmds(folder=CSRC, prefix=""):
     cmds = []
-    for src in sorted(glob.glob(os.path.join(CSRC, "*.hip"))):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+    for src in sorted(glob.glob(os.path.join(folder, "*.hip"))):
+        obj = os.path.join(BUILD_DIR, prefix + os.path.basename(src) + ".o")
         cmds.append((src, obj, [HIPCC, *COMMON, *DEVICE, "-c", src, "-o", obj]))
-    for src in sorted(glob.glob(os.path.join(CSRC, "*.cpp"))):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+    for src in sorted(glob.glob(os.path.join(folder, "*.cpp"))):
+        obj = os.path.join(BUILD_DIR, prefix + os.path.basename(src) + ".o")
         cmds.append((src, obj, [HIPCC, *COMMON, *DEVICE, "-x", "hip", "-c", src, "-o", obj]))
     return cmds
 
@@ -68,8 +71,9 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     t0 = time.time()
     cmds = _compile_cmds()
+    decode_cmds = _compile_cmds(DECODE_SRC, "decode_")
     procs = []
-    for src, obj, cmd in cmds:
+    for src, obj, cmd in cmds + decode_cmds:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
@@ -91,6 +95,10 @@ def build(verbose: bool = False) -> str:
             *[obj for _, obj, _ in cmds], "-ldl"]
     subprocess.run(link, check=True)
     os.replace(tmp, LIB_PATH)
+    tmp = DECODE_PATH + ".tmp%d" % os.getpid()
+    subprocess.run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp,
+                    *[obj for _, obj, _ in decode_cmds]], check=True)
+    os.replace(tmp, DECODE_PATH)
     tmp = OVERLAP_PATH + ".tmp%d" % os.getpid()
     # Every inner loop starts on a 64-byte boundary.  The modes' FMA loops are
     # the same nine instructions; left where the compiler put them, two of the

@@ -1,0 +1,57 @@
+// What the files of libmi_decode share: the kernels' arguments and launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "mi_decode.h"
+
+namespace mid {
+
+struct W4Args {
+  const void* x;
+  const uint32_t* qw;
+  const void* scales;
+  const uint8_t* zeros;  // nullptr: 8 everywhere
+  const void* bias;      // nullptr: none
+  void* y;
+  int64_t ldx, ldy;
+  int32_t M, N, K, group;
+  int32_t bf16;
+};
+
+struct KvArgs {
+  mi_decode_cache_t cache;
+  mi_decode_batch_t batch;
+  int32_t bf16;
+};
+
+struct AppendArgs : KvArgs {
+  mi_decode_rows_t k, v, q, q_out;
+  const float* rope;  // nullptr: no rotation
+  int64_t rope_rows;
+  int32_t rot_dim, interleaved, q_heads;
+};
+
+struct ReadArgs : KvArgs {
+  void* k_out;
+  void* v_out;
+};
+
+struct AttendArgs : KvArgs {
+  mi_decode_rows_t q, out;
+  int64_t max_len;
+  int32_t q_heads, window, sinks;
+  float scale;
+  float* ws;  // partial results, MI_DECODE_WORKSPACE_BYTES
+  int* cnt;   // arrival counters, zero between launches
+};
+
+// Each enqueues its kernel for arguments that have been checked; none is empty.
+hipError_t launch_w4(const W4Args& a, hipStream_t s);
+hipError_t launch_append(const AppendArgs& a, hipStream_t s);
+hipError_t launch_read(const ReadArgs& a, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
+
+constexpr int kCounters = 65536;
+
+}  // namespace mid
