@@ -1,76 +1,611 @@
-// Attention over the paged 8-bit cache.  One wave to a query and head: lanes
-// take positions for the logits and channels for the sum, with the running
-// maximum m and sum l of a softmax:
-//   m' = max(m, logits),  l' = l e^{m-m'} + sum e^{logit-m'},  o' = o e^{m-m'} + sum e^{logit-m'} v.
+// Attention over the paged 8-bit cache, one pass over keys and values with the
+// running maximum m and sum l of a softmax (base 2):
+//   m' = max(m, z),  l' = l 2^{m-m'} + sum 2^{z-m'},  o' = o 2^{m-m'} + sum 2^{z-m'} v.
+//
+// Rows.  The G query heads of a key-value head and a sequence's n query tokens
+// are one matrix of G n rows (row r: token r / G, head r % G) against the same
+// keys, cut into blocks of 16 NT rows.  An item is one row block of one
+// sequence and key-value head; its work is the list of 32-token tiles that any
+// of its rows sees (the sinks' tiles, then the window's).
+//
+// Split.  All items' tiles lie on one line, which the workgroups cut into equal
+// pieces whatever the sequences' lengths are.  A piece that ends inside an item
+// leaves (m, l, o) in the workspace, and the item's last workgroup to arrive
+// adds the parts in the order of the line: the same bits every time.
+//
+// A wave takes every fourth tile of a piece.  Keys are the left operand (16
+// tokens by 32 channels), so the product's columns are query rows and a lane
+// holds four tokens' logits of one row: these, rounded to binary16, are in place
+// as the right operand of the second product, whose left operand are values
+// transposed with byte permutes from 8 tokens' loads.
+//
+// Codes become binary16 operands in about one instruction each: e4m3 by the
+// conversion instruction; int8 as the subnormal (code + 128) 2^-24, which is a
+// byte in a 16-bit slot, less 128 2^-24 (packed, exact).  Leaving the offset to
+// the sums instead saves that subtraction, but costs the small results of a
+// sum whose large terms are zero: 128 of them take the place of its low bits.
 #include "device.hpp"
 
 namespace mid {
 namespace {
 
-template <int CODE, bool BF16>
-__global__ __launch_bounds__(64) void attend_kernel(AttendArgs p) {
-  const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x;
-  const Span sp = span_of(p.batch, b);
-  const int i = blockIdx.x;
-  if (i >= sp.n) return;
-  const int H = p.cache.kv_heads, D = p.cache.head_dim, ps = p.cache.page_size, kh = h / (p.q_heads / H);
-  const int64_t cap = (int64_t)p.batch.table_cols * ps;
-  const int len = (int)min((int64_t)max(p.batch.lens[b], 0), cap);
-  const int pos = len - sp.n + i;
-  __shared__ float qs[256];
-  const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + (sp.first + i) * p.q.token_stride + h * p.q.head_stride;
-  for (int d = lane; d < D; d += 64) qs[d] = from16<BF16>(q[d]) * p.scale;
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[4] = {};
-  for (int j0 = 0; j0 <= pos; j0 += 64) {
-    const int j = j0 + lane;
-    const bool seen = j <= pos && (p.window == 0 || j > pos - p.window || j < p.sinks);
-    const int page = seen ? page_of(p.cache, p.batch, b, j / ps) : -1;
-    const int64_t ph = (int64_t)page * H + kh, off = (ph * ps + j % ps) * D;
-    float logit = -INFINITY, vs = 0.f;
-    if (page >= 0) {
-      const uint8_t* k = static_cast<const uint8_t*>(p.cache.k) + off;
-      float dot = 0.f;
-      for (int d = 0; d < D; ++d) dot += qs[d] * from_code<CODE>(k[d]);
-      logit = dot * p.cache.k_scale[ph];
-      vs = p.cache.v_scale[ph];
-    }
-    float top = logit;
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const bool any = __any(page >= 0);
-    if (!any) continue;
-    const float m1 = fmaxf(m, top);
-    const float keep = m == -INFINITY ? 0.f : expf(m - m1);
-    const float w = page >= 0 ? expf(logit - m1) : 0.f;
-    float sum = w;
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-    l = l * keep + sum;
-    for (int e = 0; e < D / 64; ++e) o[e] *= keep;
-    for (int t = 0; t < 64; ++t) {
-      const int pg = __shfl(page, t);
-      if (pg < 0) continue;
-      const float wt = __shfl(w, t) * __shfl(vs, t);
-      const uint8_t* v = static_cast<const uint8_t*>(p.cache.v) + (((int64_t)pg * H + kh) * ps + (j0 + t) % ps) * D;
-      for (int e = 0; e < D / 64; ++e) o[e] += wt * from_code<CODE>(v[lane + 64 * e]);
-    }
-    m = m1;
+constexpr int kWaves = 4;
+constexpr int kTile = 32;
+constexpr float kTiny = 0x1p-24f;  // int8 codes as operands are in units of this
+
+__device__ inline f32x4 mma(h8 a, h8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// over the lanes that share lane % 16
+template <typename F>
+__device__ inline float join16(float x, F f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const uint32_t a0 = a[0], a1 = a[1];
+  const uint32_t w = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1)));
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const uint32_t b0 = b[0], b1 = b[1];
+  return f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+}
+__device__ inline float max16(float x) { return join16(x, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ inline float sum16(float x) { return join16(x, [](float a, float b) { return a + b; }); }
+__device__ inline int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+__device__ inline float lane_value(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+
+// Two bytes code + 128 in 16-bit slots as two numbers code 2^-24.
+__device__ inline uint32_t centred(uint32_t w) {
+  const _Float16 off = (_Float16)(-128.f * kTiny);
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, w) + h2{off, off});
+}
+
+// Eight codes of one token as eight numbers, in order.
+template <int CODE>
+__device__ inline h8 along(uint32_t w0, uint32_t w1) {
+  u32x4 o;
+  if constexpr (CODE == MI_DECODE_INT8) {
+    w0 ^= 0x80808080u, w1 ^= 0x80808080u;
+    o[0] = centred(__builtin_amdgcn_perm(0u, w0, 0x0c010c00u));
+    o[1] = centred(__builtin_amdgcn_perm(0u, w0, 0x0c030c02u));
+    o[2] = centred(__builtin_amdgcn_perm(0u, w1, 0x0c010c00u));
+    o[3] = centred(__builtin_amdgcn_perm(0u, w1, 0x0c030c02u));
+  } else {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true));
   }
-  uint16_t* out = static_cast<uint16_t*>(p.out.data) + (sp.first + i) * p.out.token_stride + h * p.out.head_stride;
-  for (int e = 0; e < D / 64; ++e) out[lane + 64 * e] = to16<BF16>(l == 0.f ? 0.f : o[e] / l);
+  return __builtin_bit_cast(h8, o);
+}
+
+// Channels 2 B and 2 B + 1 of eight tokens' words as eight numbers each, in token order.
+template <int CODE, int B>
+__device__ inline void across(const uint32_t (&w)[8], h8& even, h8& odd) {
+  u32x4 e, o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t0 = w[2 * i], t1 = w[2 * i + 1];
+    if constexpr (CODE == MI_DECODE_INT8) {
+      e[i] = centred(__builtin_amdgcn_perm(t1, t0, 0x0c040c00u + 0x00020002u * B));
+      o[i] = centred(__builtin_amdgcn_perm(t1, t0, 0x0c050c01u + 0x00020002u * B));
+    } else {
+      const uint32_t y = __builtin_amdgcn_perm(t1, t0, 0x05010400u + 0x02020202u * B);
+      e[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.f, false));
+      o[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.f, true));
+    }
+  }
+  even = __builtin_bit_cast(h8, e);
+  odd = __builtin_bit_cast(h8, o);
+}
+
+// One row block of one sequence.
+struct Block {
+  int first, rows;  // the sequence's first token, the block's rows
+  int r0;           // the block's first row
+  int start;        // position of the sequence's first query token
+  int plo, phi;     // positions of the block's first and last row
+  int ns, lo;       // tiles of sinks, and the first tile after them
+  int tiles;        // 0: no rows
+  __device__ int token(int t) const { return kTile * (t < ns ? t : lo + t - ns); }
+};
+__device__ inline Block block_of(const AttendArgs& p, int G, int block_rows, int blocks, int pair) {
+  Block k;
+  const int b = pair / blocks, rb = pair - b * blocks;
+  const Span sp = span_of(p.batch, b);
+  const int64_t cap = (int64_t)p.batch.table_cols * p.cache.page_size;
+  const int len = (int)min((int64_t)max(p.batch.lens[b], 0), cap);
+  k.first = sp.first;
+  k.r0 = rb * block_rows;
+  const int64_t all = (int64_t)min(sp.n, p.batch.max_tokens) * G;
+  k.rows = (int)min((int64_t)block_rows, all - k.r0);
+  k.start = len - sp.n;
+  k.plo = k.start + k.r0 / G;
+  k.phi = k.start + (k.r0 + k.rows - 1) / G;
+  k.ns = k.lo = 0;
+  if (p.window) {
+    const int lo = max(0, k.plo - p.window + 1);
+    k.lo = lo / kTile;
+    k.ns = min((int)(((int64_t)min(p.sinks, max(k.phi + 1, 0)) + kTile - 1) / kTile), k.lo);
+  }
+  k.tiles = k.rows <= 0 ? 0 : max(1, k.ns + max(k.phi, 0) / kTile + 1 - k.lo);
+  return k;
+}
+
+template <int CODE, int D, int NT>
+__global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_kernel(AttendArgs p, int blocks) {
+  constexpr int ROWS = 16 * NT, KS = D / 32, DT = D / 16, VW = D / 64;  // VW: 32-bit words of a token's values in a lane
+  constexpr int OS = D + 4;
+  __shared__ float obuf[kWaves][16][OS];
+  __shared__ float mbuf[kWaves][ROWS], lbuf[kWaves][ROWS];
+  __shared__ u32x4 qbuf[NT > 1 ? NT * KS * 64 : 1];
+  __shared__ int last_flag;
+
+  const int lane = threadIdx.x & 63, tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int H = p.cache.kv_heads, G = p.q_heads / H, ps = p.cache.page_size;
+  const int pairs = p.batch.batch * blocks;
+
+  // the line's length, and where this workgroup's piece begins
+  int64_t total = 0;
+  for (int at = 0; at < pairs; at += 64) {
+    uint32_t t = at + lane < pairs ? (uint32_t)block_of(p, G, ROWS, blocks, at + lane).tiles : 0u;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) t += (uint32_t)__shfl_xor((int)t, d);
+    total += t;
+  }
+  total *= H;
+  const int64_t each = (int64_t)((double)total / (double)(int)gridDim.x) + 1;
+  const int chunk = (int)((each + kWaves - 1) / kWaves) * kWaves;
+  const int64_t begin = (int64_t)blockIdx.x * chunk, end = min(begin + chunk, total);
+  if (begin >= end) return;
+  int pair = 0;
+  int64_t before = 0;  // tiles of the pairs before `pair`, for one head
+  for (int at = 0;; at += 64) {
+    const uint32_t mine = at + lane < pairs ? (uint32_t)block_of(p, G, ROWS, blocks, at + lane).tiles : 0u;
+    uint32_t t = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_up((int)t, d);
+      if (lane >= d) t += o;
+    }
+    const uint64_t past = __ballot((before + t) * H > begin);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      pair = at + l;
+      before += (uint32_t)lane_value((int)t, l) - (uint32_t)lane_value((int)mine, l);
+      break;
+    }
+    before += (uint32_t)lane_value((int)t, 63);
+  }
+  int64_t left = end - begin;
+  Block blk = block_of(p, G, ROWS, blocks, pair);
+  int h, s0;
+  {
+    const uint32_t off = (uint32_t)(begin - before * H);
+    h = (int)(off / (uint32_t)blk.tiles);
+    s0 = (int)(off % (uint32_t)blk.tiles);
+  }
+
+  while (true) {
+    const int s1 = (int)min((int64_t)blk.tiles, s0 + left);
+    const int b = pair / blocks;
+    const int32_t* table = p.batch.table + (int64_t)b * p.batch.table_stride;
+
+    // queries: rows as columns of the right operand, scaled by a power of two;
+    // of several 16-row tiles each wave prepares one
+    h8 qf[NT == 1 ? KS : 1];
+    float fac[NT];
+    int pos[NT];
+    __syncthreads();  // the last item's reads of shared memory are over
+    {
+      const int nt = NT == 1 ? 0 : wave;
+      const int r = blk.r0 + nt * 16 + c;
+      const bool in = nt * 16 + c < blk.rows;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + (blk.first + r / G) * p.q.token_stride +
+                          (h * G + r % G) * p.q.head_stride + 16 * g;
+      float x[KS][8], top = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        u32x4 w = {0, 0, 0, 0};
+        if (in) w = *reinterpret_cast<const u32x4*>(q + 64 * (s / 2) + 8 * (s % 2));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint16_t v = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+          x[s][e] = p.bf16 ? from16<true>(v) : from16<false>(v);
+          top = fmaxf(top, fabsf(x[s][e]));
+        }
+      }
+      // the row's largest magnitude goes to [1, 2): bf16 keeps all its bits in binary16
+      top = max16(top);
+      const int ex = top > 0.f && top < INFINITY ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) : 127;
+      const float down = __builtin_bit_cast(float, (uint32_t)min(max(254 - ex, 1), 254) << 23);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        h8 f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (_Float16)(x[s][e] * down);
+        if constexpr (NT == 1) qf[s] = f;
+        else if (nt < NT) qbuf[(nt * KS + s) * 64 + lane] = __builtin_bit_cast(u32x4, f);
+      }
+      float f = p.scale * 1.44269504088896340736f / down;
+      if (CODE == MI_DECODE_INT8) f *= 1.f / kTiny;
+      if constexpr (NT == 1) {
+        fac[0] = f;
+      } else {
+        if (nt < NT && g == 0) mbuf[0][nt * 16 + c] = f;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int n2 = 0; n2 < NT; ++n2) {
+        if (NT > 1) fac[n2] = mbuf[0][n2 * 16 + c];
+        pos[n2] = n2 * 16 + c < blk.rows ? blk.start + (blk.r0 + n2 * 16 + c) / G : -1;
+      }
+      if (NT > 1) __syncthreads();
+    }
+
+    float m[NT], l[NT], vmax = 0.f;
+    f32x4 o[NT][DT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = -INFINITY, l[nt] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[nt][d] = f32x4{0, 0, 0, 0};
+    }
+
+    // pages and scales of the wave's next 64 tiles, one to a lane, for each half of a tile
+    int pg[2];
+    float ks[2], vr[2];
+    auto lookup = [&](int tile) {
+      const int t = tile + kWaves * lane;
+      float top = 0.f;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        pg[st] = -1, ks[st] = 0.f, vr[st] = 0.f;
+        const int tok = blk.token(t) + 16 * st;
+        const bool some = t < s1 && tok <= blk.phi &&
+                          (p.window == 0 || tok + 15 > blk.plo - p.window || tok < p.sinks);
+        if (some) {
+          const int page = table[tok / ps];
+          if (page >= 0 && (int64_t)page < p.cache.pages) {
+            pg[st] = page;
+            const int64_t at = (int64_t)page * H + h;
+            ks[st] = p.cache.k_scale[at];
+            vr[st] = p.cache.v_scale[at];
+            const float a = fabsf(vr[st]);
+            if (a < INFINITY) top = fmaxf(top, a);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+      // sums are kept in units of the largest value scale so far; one that is
+      // not finite reaches the rows that see it and no others
+      float down = 1.f;
+      if (top > vmax) {
+        down = vmax / top;
+        vmax = top;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[nt][d] *= down;
+        }
+      }
+      const float unit = vmax > 0.f ? vmax : 1.f;
+      vr[0] /= unit, vr[1] /= unit;
+      return down;
+    };
+
+    u32x4 kraw[2][KS / 2];
+    uint32_t vraw[8][VW];
+    const uint32_t koff = c * D + g * 16, voff = g * 4 * D + c * (D / 16);
+    // the bytes of 16 tokens; where there is no page, readable memory that is masked later
+    auto place = [&](const void* base, int i, int tile, int st) {
+      const int page = lane_value(pg[st], i);
+      const int64_t at = (((int64_t)page * H + h) * ps + ((blk.token(tile) + 16 * st) & (ps - 1))) * D;
+      return page >= 0 ? static_cast<const uint8_t*>(base) + at : reinterpret_cast<const uint8_t*>(p.ws);
+    };
+    auto load_k = [&](int i, int tile) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint8_t* k = place(p.cache.k, i, tile, st);
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) kraw[st][j] = *reinterpret_cast<const u32x4*>(k + koff + 64 * j);
+      }
+    };
+    auto load_v = [&](int i, int tile) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint8_t* v = place(p.cache.v, i, tile, st) + voff;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (VW == 1) vraw[4 * st + e][0] = *reinterpret_cast<const uint32_t*>(v + e * D);
+          else if constexpr (VW == 2) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(v + e * D);
+            vraw[4 * st + e][0] = w[0], vraw[4 * st + e][1] = w[1];
+          } else {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(v + e * D);
+#pragma unroll
+            for (int i2 = 0; i2 < 4; ++i2) vraw[4 * st + e][i2 % VW] = w[i2];
+          }
+        }
+      }
+    };
+    auto seen = [&](int tok, int at) {
+      return tok <= at && (p.window == 0 || tok > at - p.window || tok < p.sinks);
+    };
+    int tile = s0 + wave, i = 0;
+    if (tile < s1) {
+      lookup(tile);
+      load_k(0, tile);
+      load_v(0, tile);
+    }
+    for (; tile < s1; tile += kWaves) {
+      const int tok0 = blk.token(tile);
+      const int pg0 = lane_value(pg[0], i), pg1 = lane_value(pg[1], i);
+      const float ks0 = lane_value(ks[0], i), ks1 = lane_value(ks[1], i);
+      float vr0 = lane_value(vr[0], i), vr1 = lane_value(vr[1], i);
+      const bool whole = pg0 >= 0 && pg1 >= 0 && tok0 + kTile - 1 <= blk.plo &&
+                         (p.window == 0 || tok0 > blk.phi - p.window || tok0 + kTile - 1 < p.sinks);
+      const int next = tile + kWaves;
+      if (++i == 64) {
+        i = 0;
+        const float down = lookup(next);
+        vr0 *= down, vr1 *= down;
+      }
+
+      f32x4 z[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+          z[nt][st] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        h8 kf[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+          kf[st] = along<CODE>(kraw[st][s / 2][2 * (s % 2)], kraw[st][s / 2][2 * (s % 2) + 1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          h8 q;
+          if constexpr (NT == 1) q = qf[s];
+          else q = __builtin_bit_cast(h8, qbuf[(nt * KS + s) * 64 + lane]);
+#pragma unroll
+          for (int st = 0; st < 2; ++st) z[nt][st] = mma(kf[st], q, z[nt][st]);
+        }
+        if (NT > 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      load_k(i, next);  // past the piece's end there is no page
+
+      h8 pf[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float f0 = fac[nt] * ks0, f1 = fac[nt] * ks1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[nt][0][e] *= f0, z[nt][1][e] *= f1;
+        if (!whole) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((st ? pg1 : pg0) < 0 || !seen(tok0 + 16 * st + 4 * g + e, pos[nt])) z[nt][st][e] = -INFINITY;
+        }
+        float top = fmaxf(fmaxf(fmaxf(z[nt][0][0], z[nt][0][1]), fmaxf(z[nt][0][2], z[nt][0][3])),
+                          fmaxf(fmaxf(z[nt][1][0], z[nt][1][1]), fmaxf(z[nt][1][2], z[nt][1][3])));
+        // m moves only when weights would pass 2^8, which binary16 holds as well as 1
+        if (__any(top > m[nt] + 8.f)) {
+          const float m1 = fmaxf(m[nt], max16(top));
+          const float down = m[nt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[nt] - m1);
+          m[nt] = m1;
+          l[nt] *= down;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[nt][d] *= down;
+        }
+        const float base = m[nt] == -INFINITY ? 0.f : m[nt];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float w = __builtin_amdgcn_exp2f(z[nt][st][e] - base);
+            l[nt] += w;
+            float x = w * (st ? vr1 : vr0);
+            if (!whole && z[nt][st][e] == -INFINITY) x = 0.f;
+            pf[nt][4 * st + e] = (_Float16)x;
+          }
+      }
+
+      if (CODE == MI_DECODE_E4M3 && !whole) {
+        // codes that no row sees may be NaN, and one that some rows see is NaN to those alone
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int tok = tok0 + 16 * (e / 4) + 4 * g + e % 4;
+          const bool any = (e < 4 ? pg0 : pg1) >= 0 && tok <= blk.phi &&
+                           (p.window == 0 || tok > blk.plo - p.window || tok < p.sinks);
+          bool nan = false;
+#pragma unroll
+          for (int x = 0; x < VW; ++x) {
+            if (!any) vraw[e][x] = 0;
+            nan |= (((vraw[e][x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+          }
+          const uint64_t bad = __ballot(nan);
+          if (bad) {
+            const bool mine = (bad >> (16 * g)) & 0xffff;  // the token's row has a NaN
+#pragma unroll
+            for (int x = 0; x < VW; ++x)
+              if (mine) vraw[e][x] = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              if (mine && seen(tok, pos[nt])) pf[nt][e] = (_Float16)NAN;
+          }
+        }
+      }
+      // o += V^T P^T over the tile's 32 tokens
+#pragma unroll
+      for (int x = 0; x < VW; ++x) {
+        uint32_t col[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) col[e] = CODE == MI_DECODE_INT8 ? vraw[e][x] ^ 0x80808080u : vraw[e][x];
+        h8 a0, a1, a2, a3;
+        across<CODE, 0>(col, a0, a1);
+        across<CODE, 1>(col, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          o[nt][4 * x] = mma(a0, pf[nt], o[nt][4 * x]);
+          o[nt][4 * x + 1] = mma(a1, pf[nt], o[nt][4 * x + 1]);
+          o[nt][4 * x + 2] = mma(a2, pf[nt], o[nt][4 * x + 2]);
+          o[nt][4 * x + 3] = mma(a3, pf[nt], o[nt][4 * x + 3]);
+        }
+        if (NT > 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      load_v(i, next);
+    }
+
+    // the four waves' sums to one
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float sum = sum16(l[nt]);
+      if (g == 0) mbuf[wave][nt * 16 + c] = m[nt], lbuf[wave][nt * 16 + c] = sum;
+    }
+    const bool whole_item = s0 == 0 && s1 == blk.tiles;
+    float* slot = p.ws + (int64_t)(2 * (int)blockIdx.x + (s0 == 0)) * (ROWS * (D + 2));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt * 16 >= blk.rows) break;
+      if (nt) __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int d = 0; d < DT; d += 4) {
+          f32x4 x;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            x[y] = o[nt][d + y][e] * vmax;
+            if (CODE == MI_DECODE_INT8) x[y] *= 1.f / kTiny;
+          }
+          *reinterpret_cast<f32x4*>(&obuf[wave][c][(4 * g + e) * DT + d]) = x;
+        }
+      __syncthreads();
+      for (int e = tid; e < 16 * (D / 4); e += 64 * kWaves) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4, rr = nt * 16 + row;
+        if (rr >= blk.rows) break;
+        float top = mbuf[0][rr];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, mbuf[w][rr]);
+        const float base = top == -INFINITY ? 0.f : top;
+        f32x4 x = {0, 0, 0, 0};
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(mbuf[w][rr] - base);
+          sum += f * lbuf[w][rr];
+          x += f * *reinterpret_cast<const f32x4*>(&obuf[w][row][d]);
+        }
+        if (whole_item) {
+          const int r = blk.r0 + rr;
+          uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
+                          (h * G + r % G) * p.out.head_stride + d;
+          u32x2 y = {0, 0};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float v = sum == 0.f ? 0.f : x[k] / sum;
+            y[k / 2] |= (uint32_t)(p.bf16 ? to16<true>(v) : to16<false>(v)) << (16 * (k % 2));
+          }
+          *reinterpret_cast<u32x2*>(out) = y;
+        } else {
+          *reinterpret_cast<f32x4*>(slot + rr * D + d) = x;
+          if (d == 0) slot[ROWS * D + rr] = top, slot[ROWS * D + ROWS + rr] = sum;
+        }
+      }
+    }
+
+    if (!whole_item) {
+      const int earlier = (s0 + chunk - 1) / chunk, later = (blk.tiles - s1 + chunk - 1) / chunk;
+      const int first = (int)blockIdx.x - earlier, parts = earlier + 1 + later;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) last_flag = __hip_atomic_fetch_add(p.cnt + first, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+      __syncthreads();
+      if (last_flag) {
+        __threadfence();
+        auto part = [&](int i) { return p.ws + (int64_t)(2 * (first + i) + (i == 0)) * (ROWS * (D + 2)); };
+        for (int e = tid; e < blk.rows * (D / 4); e += 64 * kWaves) {
+          const int rr = e / (D / 4), d = e % (D / 4) * 4;
+          float top = -INFINITY;
+          for (int i2 = 0; i2 < parts; ++i2) top = fmaxf(top, part(i2)[ROWS * D + rr]);
+          const float base = top == -INFINITY ? 0.f : top;
+          f32x4 x = {0, 0, 0, 0};
+          float sum = 0.f;
+          for (int i2 = 0; i2 < parts; ++i2) {
+            const float* s = part(i2);
+            const float f = __builtin_amdgcn_exp2f(s[ROWS * D + rr] - base);
+            sum += f * s[ROWS * D + ROWS + rr];
+            x += f * *reinterpret_cast<const f32x4*>(s + rr * D + d);
+          }
+          const int r = blk.r0 + rr;
+          uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
+                          (h * G + r % G) * p.out.head_stride + d;
+          u32x2 y = {0, 0};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float v = sum == 0.f ? 0.f : x[k] / sum;
+            y[k / 2] |= (uint32_t)(p.bf16 ? to16<true>(v) : to16<false>(v)) << (16 * (k % 2));
+          }
+          *reinterpret_cast<u32x2*>(out) = y;
+        }
+        if (tid == 0) __hip_atomic_store(p.cnt + first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+
+    left -= s1 - s0;
+    if (left <= 0) return;
+    s0 = 0;
+    if (++h == H) {
+      h = 0;
+      do blk = block_of(p, G, ROWS, blocks, ++pair);
+      while (blk.tiles == 0);
+    }
+  }
+}
+
+template <int CODE, int D, int NT>
+hipError_t run(const AttendArgs& a, hipStream_t s) {
+  constexpr int ROWS = 16 * NT;
+  const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
+  const int64_t blocks = (rows + ROWS - 1) / ROWS;
+  if (blocks * a.batch.batch > INT32_MAX) return hipErrorInvalidConfiguration;
+  int grid = 2 * (a.cus < 304 ? a.cus : 304);
+  static_assert(sizeof(float) * ROWS * (D + 2) * 2 * 2 * 304 <= MI_DECODE_WORKSPACE_BYTES, "partial results");
+  const double tiles = (double)blocks * a.batch.batch * a.cache.kv_heads * (a.max_len / kTile + 1);
+  if (tiles < grid) grid = (int)tiles;
+  attend_kernel<CODE, D, NT><<<grid, 64 * kWaves, 0, s>>>(a, (int)blocks);
+  return hipGetLastError();
+}
+
+template <int CODE, int D>
+hipError_t rows_of(const AttendArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
+  if (rows <= 16) return run<CODE, D, 1>(a, s);
+  if constexpr (D == 256) {
+    return run<CODE, D, 2>(a, s);
+  } else {
+    if (rows <= 32) return run<CODE, D, 2>(a, s);
+    if (rows <= 48) return run<CODE, D, 3>(a, s);
+    return run<CODE, D, 4>(a, s);
+  }
+}
+
+template <int CODE>
+hipError_t dims_of(const AttendArgs& a, hipStream_t s) {
+  if (a.cache.head_dim == 64) return rows_of<CODE, 64>(a, s);
+  if (a.cache.head_dim == 128) return rows_of<CODE, 128>(a, s);
+  return rows_of<CODE, 256>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid(a.batch.max_tokens, a.q_heads, a.batch.batch);
-  if (a.cache.code == MI_DECODE_INT8) {
-    if (a.bf16) attend_kernel<MI_DECODE_INT8, true><<<grid, 64, 0, s>>>(a);
-    else attend_kernel<MI_DECODE_INT8, false><<<grid, 64, 0, s>>>(a);
-  } else {
-    if (a.bf16) attend_kernel<MI_DECODE_E4M3, true><<<grid, 64, 0, s>>>(a);
-    else attend_kernel<MI_DECODE_E4M3, false><<<grid, 64, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  return a.cache.code == MI_DECODE_INT8 ? dims_of<MI_DECODE_INT8>(a, s) : dims_of<MI_DECODE_E4M3>(a, s);
 }
 
 }  // namespace mid

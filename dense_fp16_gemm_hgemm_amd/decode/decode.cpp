@@ -41,6 +41,7 @@ Extent extent(const mi_decode_rows_t& r, int64_t tokens, int64_t heads, int64_t 
 
 struct mi_decode_ctx {
   int device = -1;
+  int cus = 0;
   bool no_device = false;
   float* ws = nullptr;
   int* cnt = nullptr;
@@ -129,6 +130,7 @@ mi_decode_status_t mi_decode_create(mi_decode_handle_t* out, uint32_t flags) {
     delete h;
     return MI_DECODE_ERR_HIP;
   }
+  h->cus = prop.multiProcessorCount;
   h->ws = static_cast<float*>(ws);
   h->cnt = static_cast<int*>(cnt);
   *out = h;
@@ -310,6 +312,7 @@ mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cac
   a.scale = scale;
   a.ws = h->ws;
   a.cnt = h->cnt;
+  a.cus = h->cus;
   DeviceGuard g(h->device);
   return done(h, launch_attend(a, (hipStream_t)stream));
 }

@@ -44,6 +44,7 @@ struct AttendArgs : KvArgs {
   float scale;
   float* ws;  // partial results, MI_DECODE_WORKSPACE_BYTES
   int* cnt;   // arrival counters, zero between launches
+  int cus;    // the device's compute units
 };
 
 // Each enqueues its kernel for arguments that have been checked; none is empty.
