@@ -31,6 +31,9 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;
+constexpr int kItem = 16;  // what starting and ending an item costs, in tiles
+constexpr int kRsrcWord3 = 0x00020000;
+constexpr int kDeviceScope = 16;  // cache policy SC1
 constexpr float kTiny = 0x1p-24f;  // int8 codes as operands are in units of this
 
 __device__ inline f32x4 mma(h8 a, h8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
@@ -106,11 +109,23 @@ struct Block {
   int plo, phi;     // positions of the block's first and last row
   int ns, lo;       // tiles of sinks, and the first tile after them
   int tiles;        // 0: no rows
+  int b;            // the sequence
   __device__ int token(int t) const { return kTile * (t < ns ? t : lo + t - ns); }
+  __device__ Block of_lane(int l) const {
+    Block k;
+    k.first = __builtin_amdgcn_readlane(first, l), k.rows = __builtin_amdgcn_readlane(rows, l);
+    k.r0 = __builtin_amdgcn_readlane(r0, l), k.start = __builtin_amdgcn_readlane(start, l);
+    k.plo = __builtin_amdgcn_readlane(plo, l), k.phi = __builtin_amdgcn_readlane(phi, l);
+    k.ns = __builtin_amdgcn_readlane(ns, l), k.lo = __builtin_amdgcn_readlane(lo, l);
+    k.tiles = __builtin_amdgcn_readlane(tiles, l), k.b = __builtin_amdgcn_readlane(b, l);
+    return k;
+  }
 };
-__device__ inline Block block_of(const AttendArgs& p, int G, int block_rows, int blocks, int pair) {
-  Block k;
-  const int b = pair / blocks, rb = pair - b * blocks;
+__device__ inline Block block_of(const AttendArgs& p, int G, int block_rows, int blocks, int pair, int pairs) {
+  Block k = {};
+  if (pair >= pairs) return k;
+  const int b = blocks == 1 ? pair : pair / blocks, rb = pair - b * blocks;
+  k.b = b;
   const Span sp = span_of(p.batch, b);
   const int64_t cap = (int64_t)p.batch.table_cols * p.cache.page_size;
   const int len = (int)min((int64_t)max(p.batch.lens[b], 0), cap);
@@ -121,7 +136,6 @@ __device__ inline Block block_of(const AttendArgs& p, int G, int block_rows, int
   k.start = len - sp.n;
   k.plo = k.start + k.r0 / G;
   k.phi = k.start + (k.r0 + k.rows - 1) / G;
-  k.ns = k.lo = 0;
   if (p.window) {
     const int lo = max(0, k.plo - p.window + 1);
     k.lo = lo / kTile;
@@ -146,153 +160,119 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
   const int H = p.cache.kv_heads, G = p.q_heads / H, ps = p.cache.page_size;
   const int pairs = p.batch.batch * blocks;
 
-  // the line's length, and where this workgroup's piece begins
+  // the line's length, and where this workgroup's piece begins; lane i knows
+  // row block `at` + i, and the wave takes its numbers from there
+  int at = 0;
+  Block mine = block_of(p, G, ROWS, blocks, lane, pairs);
   int64_t total = 0;
-  for (int at = 0; at < pairs; at += 64) {
-    uint32_t t = at + lane < pairs ? (uint32_t)block_of(p, G, ROWS, blocks, at + lane).tiles : 0u;
+  uint32_t ahead = 0;  // line of the blocks up to the lane's own, for one head
+  auto extend = [&]() {
+    ahead = mine.tiles > 0 ? (uint32_t)mine.tiles + kItem : 0u;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) t += (uint32_t)__shfl_xor((int)t, d);
-    total += t;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_up((int)ahead, d);
+      if (lane >= d) ahead += o;
+    }
+    return (uint32_t)lane_value((int)ahead, 63);
+  };
+  while (true) {
+    total += extend();
+    if (at + 64 >= pairs) break;
+    at += 64;
+    mine = block_of(p, G, ROWS, blocks, at + lane, pairs);
   }
   total *= H;
   const int64_t each = (int64_t)((double)total / (double)(int)gridDim.x) + 1;
   const int chunk = (int)((each + kWaves - 1) / kWaves) * kWaves;
   const int64_t begin = (int64_t)blockIdx.x * chunk, end = min(begin + chunk, total);
   if (begin >= end) return;
-  int pair = 0;
-  int64_t before = 0;  // tiles of the pairs before `pair`, for one head
-  for (int at = 0;; at += 64) {
-    const uint32_t mine = at + lane < pairs ? (uint32_t)block_of(p, G, ROWS, blocks, at + lane).tiles : 0u;
-    uint32_t t = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t o = (uint32_t)__shfl_up((int)t, d);
-      if (lane >= d) t += o;
+  int64_t before = 0;
+  if (at > 0) {
+    at = 0;
+    while (true) {
+      mine = block_of(p, G, ROWS, blocks, at + lane, pairs);
+      const uint32_t more = extend();
+      if ((before + more) * H > begin) break;
+      before += more;
+      at += 64;
     }
-    const uint64_t past = __ballot((before + t) * H > begin);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      pair = at + l;
-      before += (uint32_t)lane_value((int)t, l) - (uint32_t)lane_value((int)mine, l);
-      break;
-    }
-    before += (uint32_t)lane_value((int)t, 63);
+  }
+  int who = __builtin_ctzll(__ballot((before + ahead) * H > begin));  // the block's lane
+  Block blk = mine.of_lane(who);
+  int h, v0;  // head, and where in the item's line the piece begins
+  {
+    const uint32_t off = (uint32_t)(begin - (before + (uint32_t)lane_value((int)ahead, who) - (blk.tiles + kItem)) * H);
+    h = (int)(off / (uint32_t)(blk.tiles + kItem));
+    v0 = (int)(off % (uint32_t)(blk.tiles + kItem));
   }
   int64_t left = end - begin;
-  Block blk = block_of(p, G, ROWS, blocks, pair);
-  int h, s0;
-  {
-    const uint32_t off = (uint32_t)(begin - before * H);
-    h = (int)(off / (uint32_t)blk.tiles);
-    s0 = (int)(off % (uint32_t)blk.tiles);
-  }
 
-  while (true) {
-    const int s1 = (int)min((int64_t)blk.tiles, s0 + left);
-    const int b = pair / blocks;
-    const int32_t* table = p.batch.table + (int64_t)b * p.batch.table_stride;
+  // a part: sums of ROWS x D, then m and l of each row
+  constexpr uint32_t kPart = 4 * ROWS * (D + 2);
+  const auto parts_at = __builtin_amdgcn_make_buffer_rsrc(p.ws, (short)0, (int)MI_DECODE_WORKSPACE_BYTES, kRsrcWord3);
 
-    // queries: rows as columns of the right operand, scaled by a power of two;
-    // of several 16-row tiles each wave prepares one
-    h8 qf[NT == 1 ? KS : 1];
-    float fac[NT];
-    int pos[NT];
-    __syncthreads();  // the last item's reads of shared memory are over
+  auto item = [&](const Block& blk, int h, int s0, int s1) {
+    const int32_t* table = p.batch.table + (int64_t)blk.b * p.batch.table_stride;
+
+    // the block's queries: rows as columns of the right operand.  Of several
+    // 16-row tiles each wave prepares one
+    const int qt = NT == 1 ? 0 : wave;
+    u32x4 qraw[KS];
     {
-      const int nt = NT == 1 ? 0 : wave;
-      const int r = blk.r0 + nt * 16 + c;
-      const bool in = nt * 16 + c < blk.rows;
+      const int r = blk.r0 + qt * 16 + c;
       const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + (blk.first + r / G) * p.q.token_stride +
                           (h * G + r % G) * p.q.head_stride + 16 * g;
-      float x[KS][8], top = 0.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        u32x4 w = {0, 0, 0, 0};
-        if (in) w = *reinterpret_cast<const u32x4*>(q + 64 * (s / 2) + 8 * (s % 2));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint16_t v = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
-          x[s][e] = p.bf16 ? from16<true>(v) : from16<false>(v);
-          top = fmaxf(top, fabsf(x[s][e]));
-        }
+        qraw[s] = u32x4{0, 0, 0, 0};
+        if (qt * 16 + c < blk.rows) qraw[s] = *reinterpret_cast<const u32x4*>(q + 64 * (s / 2) + 8 * (s % 2));
       }
-      // the row's largest magnitude goes to [1, 2): bf16 keeps all its bits in binary16
-      top = max16(top);
-      const int ex = top > 0.f && top < INFINITY ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) : 127;
-      const float down = __builtin_bit_cast(float, (uint32_t)min(max(254 - ex, 1), 254) << 23);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        h8 f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (_Float16)(x[s][e] * down);
-        if constexpr (NT == 1) qf[s] = f;
-        else if (nt < NT) qbuf[(nt * KS + s) * 64 + lane] = __builtin_bit_cast(u32x4, f);
-      }
-      float f = p.scale * 1.44269504088896340736f / down;
-      if (CODE == MI_DECODE_INT8) f *= 1.f / kTiny;
-      if constexpr (NT == 1) {
-        fac[0] = f;
-      } else {
-        if (nt < NT && g == 0) mbuf[0][nt * 16 + c] = f;
-        __syncthreads();
-      }
-#pragma unroll
-      for (int n2 = 0; n2 < NT; ++n2) {
-        if (NT > 1) fac[n2] = mbuf[0][n2 * 16 + c];
-        pos[n2] = n2 * 16 + c < blk.rows ? blk.start + (blk.r0 + n2 * 16 + c) / G : -1;
-      }
-      if (NT > 1) __syncthreads();
-    }
-
-    float m[NT], l[NT], vmax = 0.f;
-    f32x4 o[NT][DT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt] = -INFINITY, l[nt] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[nt][d] = f32x4{0, 0, 0, 0};
     }
 
     // pages and scales of the wave's next 64 tiles, one to a lane, for each half of a tile
     int pg[2];
-    float ks[2], vr[2];
-    auto lookup = [&](int tile) {
+    float ks[2], vr[2], vmax = 0.f;
+    auto pages = [&](int tile) {
       const int t = tile + kWaves * lane;
-      float top = 0.f;
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        pg[st] = -1, ks[st] = 0.f, vr[st] = 0.f;
         const int tok = blk.token(t) + 16 * st;
         const bool some = t < s1 && tok <= blk.phi &&
                           (p.window == 0 || tok + 15 > blk.plo - p.window || tok < p.sinks);
-        if (some) {
-          const int page = table[tok / ps];
-          if (page >= 0 && (int64_t)page < p.cache.pages) {
-            pg[st] = page;
-            const int64_t at = (int64_t)page * H + h;
-            ks[st] = p.cache.k_scale[at];
-            vr[st] = p.cache.v_scale[at];
-            const float a = fabsf(vr[st]);
-            if (a < INFINITY) top = fmaxf(top, a);
-          }
+        pg[st] = -1;
+        if (some) pg[st] = table[tok / ps];
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+        if (pg[st] < 0 || (int64_t)pg[st] >= p.cache.pages) pg[st] = -1;
+    };
+    auto scales = [&]() {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        ks[st] = 0.f, vr[st] = 0.f;
+        if (pg[st] >= 0) {
+          const int64_t at = (int64_t)pg[st] * H + h;
+          ks[st] = p.cache.k_scale[at];
+          vr[st] = p.cache.v_scale[at];
         }
+      }
+    };
+    // Sums are kept in units of the largest value scale so far, and vr becomes
+    // the scales in that unit; one that is not finite reaches the rows that see
+    // it and no others.  Returns what sums in the old unit are multiplied by.
+    auto unit = [&]() {
+      float top = 0.f;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const float a = fabsf(vr[st]);
+        if (a < INFINITY) top = fmaxf(top, a);
       }
 #pragma unroll
       for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-      // sums are kept in units of the largest value scale so far; one that is
-      // not finite reaches the rows that see it and no others
       float down = 1.f;
-      if (top > vmax) {
-        down = vmax / top;
-        vmax = top;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[nt][d] *= down;
-        }
-      }
-      const float unit = vmax > 0.f ? vmax : 1.f;
-      vr[0] /= unit, vr[1] /= unit;
+      if (top > vmax) down = vmax / top, vmax = top;
+      const float u = vmax > 0.f ? vmax : 1.f;
+      vr[0] /= u, vr[1] /= u;
       return down;
     };
 
@@ -335,11 +315,63 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       return tok <= at && (p.window == 0 || tok > at - p.window || tok < p.sinks);
     };
     int tile = s0 + wave, i = 0;
-    if (tile < s1) {
-      lookup(tile);
-      load_k(0, tile);
-      load_v(0, tile);
+    pages(tile);
+    scales();
+    load_k(0, tile);
+    load_v(0, tile);
+
+    h8 qf[NT == 1 ? KS : 1];
+    float fac[NT];
+    int pos[NT];
+    __syncthreads();  // the last item's reads of shared memory are over
+    {
+      // the row's largest magnitude goes to [1, 2): bf16 keeps all its bits in binary16
+      float x[KS][8], top = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint16_t v = (uint16_t)(qraw[s][e / 2] >> (16 * (e % 2)));
+          x[s][e] = p.bf16 ? from16<true>(v) : from16<false>(v);
+          top = fmaxf(top, fabsf(x[s][e]));
+        }
+      top = max16(top);
+      const int ex = top > 0.f && top < INFINITY ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) : 127;
+      const float down = __builtin_bit_cast(float, (uint32_t)min(max(254 - ex, 1), 254) << 23);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        h8 f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (_Float16)(x[s][e] * down);
+        if constexpr (NT == 1) qf[s] = f;
+        else if (qt < NT) qbuf[(qt * KS + s) * 64 + lane] = __builtin_bit_cast(u32x4, f);
+      }
+      float f = p.scale * 1.44269504088896340736f / down;
+      if (CODE == MI_DECODE_INT8) f *= 1.f / kTiny;
+      if constexpr (NT == 1) {
+        fac[0] = f;
+      } else {
+        if (qt < NT && g == 0) mbuf[0][qt * 16 + c] = f;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (NT > 1) fac[nt] = mbuf[0][nt * 16 + c];
+        pos[nt] = nt * 16 + c < blk.rows ? blk.start + (blk.r0 + nt * 16 + c) / G : -1;
+      }
+      if (NT > 1) __syncthreads();
     }
+
+    float m[NT], l[NT];
+    f32x4 o[NT][DT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = -INFINITY, l[nt] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[nt][d] = f32x4{0, 0, 0, 0};
+    }
+
+    unit();
     for (; tile < s1; tile += kWaves) {
       const int tok0 = blk.token(tile);
       const int pg0 = lane_value(pg[0], i), pg1 = lane_value(pg[1], i);
@@ -350,8 +382,14 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       const int next = tile + kWaves;
       if (++i == 64) {
         i = 0;
-        const float down = lookup(next);
+        pages(next);
+        scales();
+        const float down = unit();
         vr0 *= down, vr1 *= down;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[nt][d] *= down;
       }
 
       f32x4 z[NT][2];
@@ -461,6 +499,19 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       load_v(i, next);
     }
 
+    auto store = [&](int rr, int d, f32x4 x, float sum) {
+      const int r = blk.r0 + rr;
+      uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
+                      (h * G + r % G) * p.out.head_stride + d;
+      u32x2 y = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float v = sum == 0.f ? 0.f : x[k] / sum;
+        y[k / 2] |= (uint32_t)(p.bf16 ? to16<true>(v) : to16<false>(v)) << (16 * (k % 2));
+      }
+      *reinterpret_cast<u32x2*>(out) = y;
+    };
+
     // the four waves' sums to one
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -468,7 +519,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       if (g == 0) mbuf[wave][nt * 16 + c] = m[nt], lbuf[wave][nt * 16 + c] = sum;
     }
     const bool whole_item = s0 == 0 && s1 == blk.tiles;
-    float* slot = p.ws + (int64_t)(2 * (int)blockIdx.x + (s0 == 0)) * (ROWS * (D + 2));
+    const uint32_t slot = (uint32_t)(2 * blockIdx.x + (s0 == 0)) * kPart;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (nt * 16 >= blk.rows) break;
@@ -502,19 +553,12 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
           x += f * *reinterpret_cast<const f32x4*>(&obuf[w][row][d]);
         }
         if (whole_item) {
-          const int r = blk.r0 + rr;
-          uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
-                          (h * G + r % G) * p.out.head_stride + d;
-          u32x2 y = {0, 0};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float v = sum == 0.f ? 0.f : x[k] / sum;
-            y[k / 2] |= (uint32_t)(p.bf16 ? to16<true>(v) : to16<false>(v)) << (16 * (k % 2));
-          }
-          *reinterpret_cast<u32x2*>(out) = y;
+          store(rr, d, x, sum);
         } else {
-          *reinterpret_cast<f32x4*>(slot + rr * D + d) = x;
-          if (d == 0) slot[ROWS * D + rr] = top, slot[ROWS * D + ROWS + rr] = sum;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), parts_at, slot + 4 * (rr * D + d), 0, kDeviceScope);
+          if (d == 0)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{top, sum}), parts_at,
+                                                  slot + 4 * (ROWS * D + 2 * rr), 0, kDeviceScope);
         }
       }
     }
@@ -522,49 +566,99 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     if (!whole_item) {
       const int earlier = (s0 + chunk - 1) / chunk, later = (blk.tiles - s1 + chunk - 1) / chunk;
       const int first = (int)blockIdx.x - earlier, parts = earlier + 1 + later;
-      __threadfence();
+      // Workgroups of one item run on XCDs whose L2 caches are not coherent.
+      // Parts are stored and loaded with device scope, past those caches, and
+      // counted when their stores are acknowledged; fences would write back
+      // and drop whole caches instead (15 to 25 us between the two stores).
+      __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xf << 8));  // vmcnt(0)
       __syncthreads();
-      if (tid == 0) last_flag = __hip_atomic_fetch_add(p.cnt + first, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+      if (tid == 0) last_flag = __hip_atomic_fetch_add(p.cnt + first, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
       __syncthreads();
       if (last_flag) {
-        __threadfence();
-        auto part = [&](int i) { return p.ws + (int64_t)(2 * (first + i) + (i == 0)) * (ROWS * (D + 2)); };
-        for (int e = tid; e < blk.rows * (D / 4); e += 64 * kWaves) {
+        auto part = [&](int n) { return (uint32_t)(2 * (first + n) + (n == 0)) * kPart; };
+        // A thread adds four channels of a row over every groups-th part; where
+        // there are few rows, groups of threads share the parts.  Loads of
+        // several parts are in flight at a time: one after the other, a part
+        // costs the memory's latency (32 parts of 4 rows: 45 us).
+        const int all = blk.rows * (D / 4);
+        int groups = 1;
+        while (groups < 8 && 2 * groups * all <= 64 * kWaves && 2 * groups <= parts) groups *= 2;
+        const int per = 64 * kWaves / groups, grp = tid / per;
+        for (int e = tid % per; e < all; e += per) {
           const int rr = e / (D / 4), d = e % (D / 4) * 4;
-          float top = -INFINITY;
-          for (int i2 = 0; i2 < parts; ++i2) top = fmaxf(top, part(i2)[ROWS * D + rr]);
-          const float base = top == -INFINITY ? 0.f : top;
+          float top = -INFINITY, sum = 0.f;
           f32x4 x = {0, 0, 0, 0};
-          float sum = 0.f;
-          for (int i2 = 0; i2 < parts; ++i2) {
-            const float* s = part(i2);
-            const float f = __builtin_amdgcn_exp2f(s[ROWS * D + rr] - base);
-            sum += f * s[ROWS * D + ROWS + rr];
-            x += f * *reinterpret_cast<const f32x4*>(s + rr * D + d);
-          }
-          const int r = blk.r0 + rr;
-          uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
-                          (h * G + r % G) * p.out.head_stride + d;
-          u32x2 y = {0, 0};
+          for (int n = grp; n < parts; n += 8 * groups) {
+            float pm[8], pl[8];
+            f32x4 px[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float v = sum == 0.f ? 0.f : x[k] / sum;
-            y[k / 2] |= (uint32_t)(p.bf16 ? to16<true>(v) : to16<false>(v)) << (16 * (k % 2));
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t s = part(min(n + k * groups, parts - 1));
+              const f32x2 ml = __builtin_bit_cast(
+                  f32x2, __builtin_amdgcn_raw_buffer_load_b64(parts_at, s + 4 * (ROWS * D + 2 * rr), 0, kDeviceScope));
+              pm[k] = ml[0], pl[k] = ml[1];
+              px[k] = __builtin_bit_cast(
+                  f32x4, __builtin_amdgcn_raw_buffer_load_b128(parts_at, s + 4 * (rr * D + d), 0, kDeviceScope));
+            }
+            float t1 = top;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t1 = fmaxf(t1, pm[k]);
+            const float base = t1 == -INFINITY ? 0.f : t1, down = __builtin_amdgcn_exp2f(top - base);
+            top = t1, x *= down, sum *= down;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (n + k * groups >= parts) break;
+              const float f = __builtin_amdgcn_exp2f(pm[k] - base);
+              sum += f * pl[k];
+              x += f * px[k];
+            }
           }
-          *reinterpret_cast<u32x2*>(out) = y;
+          if (groups > 1) {  // then every thread has one element at most
+            float* mine = &obuf[0][0][0] + 6 * tid;
+            mine[0] = top, mine[1] = sum;
+            mine[2] = x[0], mine[3] = x[1], mine[4] = x[2], mine[5] = x[3];
+          } else {
+            store(rr, d, x, sum);
+          }
+        }
+        if (groups > 1) {
+          __syncthreads();
+          for (int e = tid; e < all; e += 64 * kWaves) {
+            float top = -INFINITY, sum = 0.f;
+            f32x4 x = {0, 0, 0, 0};
+            for (int k = 0; k < groups; ++k) top = fmaxf(top, (&obuf[0][0][0])[6 * (k * per + e)]);
+            const float base = top == -INFINITY ? 0.f : top;
+            for (int k = 0; k < groups; ++k) {
+              const float* s = &obuf[0][0][0] + 6 * (k * per + e);
+              const float f = __builtin_amdgcn_exp2f(s[0] - base);
+              sum += f * s[1];
+              x += f * f32x4{s[2], s[3], s[4], s[5]};
+            }
+            store(e / (D / 4), e % (D / 4) * 4, x, sum);
+          }
         }
         if (tid == 0) __hip_atomic_store(p.cnt + first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
 
-    left -= s1 - s0;
+  };
+
+  while (true) {
+    const int v1 = (int)min((int64_t)(blk.tiles + kItem), v0 + left);
+    const int s0 = max(v0 - kItem, 0), s1 = max(v1 - kItem, 0);
+    if (s1 > s0) item(blk, h, s0, s1);
+    left -= v1 - v0;
     if (left <= 0) return;
-    s0 = 0;
-    if (++h == H) {
-      h = 0;
-      do blk = block_of(p, G, ROWS, blocks, ++pair);
-      while (blk.tiles == 0);
-    }
+    v0 = 0;
+    if (++h < H) continue;
+    h = 0;
+    do {
+      if (++who == 64) {
+        who = 0, at += 64;
+        mine = block_of(p, G, ROWS, blocks, at + lane, pairs);
+      }
+      blk = mine.of_lane(who);
+    } while (blk.tiles == 0);
   }
 }
 
@@ -574,7 +668,7 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
   const int64_t blocks = (rows + ROWS - 1) / ROWS;
   if (blocks * a.batch.batch > INT32_MAX) return hipErrorInvalidConfiguration;
-  int grid = 2 * (a.cus < 304 ? a.cus : 304);
+  int grid = (NT * D >= 256 ? 1 : 2) * (a.cus < 304 ? a.cus : 304);
   static_assert(sizeof(float) * ROWS * (D + 2) * 2 * 2 * 304 <= MI_DECODE_WORKSPACE_BYTES, "partial results");
   const double tiles = (double)blocks * a.batch.batch * a.cache.kv_heads * (a.max_len / kTile + 1);
   if (tiles < grid) grid = (int)tiles;
