@@ -198,6 +198,8 @@ mi_decode_status_t mi_decode_w4_linear(mi_decode_handle_t h, mi_decode_dtype_t d
   a.N = (int32_t)N;
   a.K = (int32_t)K;
   a.group = (int32_t)(group < INT32_MAX ? group : INT32_MAX / 32 * 32);
+  a.cus = h->cus;
+  a.group_inv = a.group == 32 ? UINT32_MAX : (uint32_t)((uint64_t(1) << 32) / (a.group / 32));
   a.bf16 = dtype == MI_DECODE_BF16;
   DeviceGuard g(h->device);
   return done(h, launch_w4(a, (hipStream_t)stream));

@@ -16,6 +16,8 @@ struct W4Args {
   void* y;
   int64_t ldx, ldy;
   int32_t M, N, K, group;
+  int32_t cus;         // the device's compute units
+  uint32_t group_inv;  // floor(2^32 / (group / 32)), 2^32 - 1 for 32
   int32_t bf16;
 };
 

@@ -1,12 +1,19 @@
 // Linear layer with 4-bit weights for few tokens:
 //   y[m][n] = sum_g s[n][g] * sum_{k in g} x[m][k] (c[n][k] - z[n][g]) + bias[n].
 //
-// A workgroup owns 16 NT rows of weights and all its waves split K: wave w
+// A workgroup owns 16 NT rows of weights and its waves split K: wave w of W
 // takes the 128-column blocks w, w + W, w + 2 W, ..., each one contiguous KiB
 // (a 16-byte load per lane) per 16 rows, which is the operand of four 16x16x32
 // matrix instructions.  U blocks are in flight per wave, and the waves' sums
 // are added in wave order through LDS at the end: one pass over the weights,
-// one launch, the same bits every time.
+// one launch, the same bits every time.  W is as large as lets every workgroup
+// run at once (7 x 5003 x 4072: 8.1 us; with 12 waves and two rounds 11.4).
+//
+// Bounds, measured with weights that change from call to call: up to 8 tokens
+// latency and then the weights' bytes (1 x 4096 x 4096 4.8 us, of which an
+// empty launch takes 3.4; 1 x 32768 x 4096 17.7 us, 3.9 TB/s); from 32 tokens
+// the unpacking and the groups' sums, about 290 vector instructions beside 40
+// matrix ones for 128 columns (64 x 14336 x 4096 18.7 us).
 //
 // Codes become matrix operands without arithmetic: code c placed under the
 // exponent of 16 is the number 16 + c (fp16: bits 6..9 of 0x4c00, bf16: bits
@@ -34,81 +41,104 @@ __device__ inline f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
 }
 
-// Eight codes as eight numbers 16 + c, in k order.
+// Eight codes as eight numbers 16 + c, in k order: a shift and an and-or make
+// two.  The and-or takes one constant from a scalar register at most, so the
+// exponent's bits come in a vector register.
 template <bool BF16>
-__device__ inline u32x4 unpack(uint32_t w) {
+__device__ inline u32x4 unpack(uint32_t w, uint32_t base) {
   if constexpr (BF16) {
-    constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;
+    constexpr uint32_t mask = 0x00780078u;
     return u32x4{(w << 3 & mask) | base, (w >> 1 & mask) | base, (w >> 5 & mask) | base, (w >> 9 & mask) | base};
   } else {
-    constexpr uint32_t mask = 0x03c003c0u, base = 0x4c004c00u;
+    constexpr uint32_t mask = 0x03c003c0u;
     return u32x4{(w << 6 & mask) | base, (w << 2 & mask) | base, (w >> 2 & mask) | base, (w >> 6 & mask) | base};
   }
 }
 
 // MT x NT tiles of 16 tokens by 16 rows of weights to a wave, U blocks of 128
-// columns in flight.  PER: matrix instructions (32 columns each) to a group's
-// sum.  WIDE: x's rows are 16-byte aligned and of whole 16-byte pieces.
-template <bool BF16, int MT, int NT, int U, int PER, bool WIDE>
-__global__ __launch_bounds__(512) void w4_kernel(W4Args p) {
+// columns in flight.  MW waves share a block and take 16 MT tokens each; the
+// other way round, waves that differ in K add their sums.  PER: matrix
+// instructions (32 columns each) to a group's sum.  R: loads of 4 tokens that
+// hold a wave's tokens.  WIDE: x's rows are 16-byte aligned and of whole
+// 16-byte pieces.
+//
+// x comes in rows of 256 bytes (16 lanes), and goes through a piece of shared
+// memory that belongs to the wave: loaded as the matrix instruction wants it,
+// neighbouring lanes are in different rows, and each such load takes as many
+// cache lookups as it has lanes (16 x 4096 x 11008:
+// 15.6 us, through shared memory 12.7).
+template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX, bool WIDE>
+__global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   constexpr int FL = 4 / PER;  // group sums to a block
   extern __shared__ float red[];
-  const int lane = threadIdx.x & 63, W = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, KW = (int)(blockDim.x >> 6) / MW;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave / MW, mw = wave % MW;
   const int r = lane & 15, c = lane >> 4;
   const int NB = (p.N + 15) >> 4, KB = (p.K + 127) >> 7;
   const int64_t np = (int64_t)NB * 16;
-  const int nb0 = blockIdx.x * NT, m0 = blockIdx.y * (16 * MT);
+  const int nb0 = blockIdx.x * NT, m0 = blockIdx.y * (16 * MT * MW) + mw * (16 * MT);
 
-  const u32x4* wp[NT];
-  int64_t sn[NT];
+  const u32x4* wp[NT];  // the tile row's first entry, the same in every lane
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int nb = min(nb0 + t, NB - 1);
-    wp[t] = reinterpret_cast<const u32x4*>(p.qw) + (int64_t)nb * KB * 64 + lane;
-    sn[t] = nb * 16 + r;
-  }
+  for (int t = 0; t < NT; ++t)
+    wp[t] = reinterpret_cast<const u32x4*>(p.qw) + (int64_t)min(nb0 + t, NB - 1) * KB * 64;
   const uint16_t* xb = static_cast<const uint16_t*>(p.x) + m0 * p.ldx;
-  uint32_t xo[MT];  // byte offset of the lane's row, or out of range
+  // lane l holds 16-byte piece l % 16 of tokens l / 16, l / 16 + 4, ...
+  const int xrow = lane >> 4, xcol = lane & 15;
+  uint32_t xo[R];  // byte offset of the lane's row and column, or out of range
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xo[m] = m0 + m * 16 + r < p.M ? (uint32_t)((m * 16 + r) * p.ldx * 2) : kOOB;
+  for (int i = 0; i < R; ++i)
+    xo[i] = m0 + 4 * i + xrow < p.M ? (uint32_t)((4 * i + xrow) * p.ldx * 2 + xcol * 16) : kOOB;
   const auto xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(xb), (short)0, (int)0x7fffffff, kRsrcWord3);
+  // the wave's [16 MT][16] pieces; piece q of row i lies at q ^ (i % 16), so
+  // that eight rows' pieces of one column do not meet in a bank
+  u32x4* xs = reinterpret_cast<u32x4*>(red) + wave * (MT * 256);
+#pragma unroll
+  for (int i = R; i < 4 * MT; ++i) xs[(4 * i + xrow) * 16 + xcol] = u32x4{0, 0, 0, 0};
 
-  u32x4 wq[U][NT], xq[U][4][MT];
+  // without zeros their loads go to the scales and are not used: a branch
+  // around them would make every later wait a wait for all loads
+  const uint8_t* zp = p.zeros ? p.zeros : static_cast<const uint8_t*>(p.scales);
+  const bool has_z = p.zeros != nullptr;
+
+  u32x4 wq[U][NT], xq[U][R];
   uint16_t sq[U][FL][NT];
   uint8_t zq[U][FL][NT];
 
   auto load = [&](int u, int kb) {
     const int at = min(kb, KB - 1);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) wq[u][t] = wp[t][(int64_t)at * 64];
+    for (int t = 0; t < NT; ++t) wq[u][t] = wp[t][(int64_t)at * 64 + lane];
 #pragma unroll
     for (int f = 0; f < FL; ++f) {
-      const int g = min(at * 128 + f * (32 * PER), p.K - 1) / p.group;
+      // the 32-column unit over the group's units: a product by the
+      // reciprocal is the quotient or one below it
+      const uint32_t unit = min(at * 4 + f * PER, (p.K - 1) >> 5);
+      uint32_t g = __umulhi(unit, p.group_inv);
+      if ((g + 1) * (uint32_t)(p.group >> 5) <= unit) ++g;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        sq[u][f][t] = static_cast<const uint16_t*>(p.scales)[g * np + sn[t]];
-        zq[u][f][t] = p.zeros ? p.zeros[g * np + sn[t]] : 8;
+        const int64_t row = g * np + min(nb0 + t, NB - 1) * 16;
+        sq[u][f][t] = (static_cast<const uint16_t*>(p.scales) + row)[r];
+        zq[u][f][t] = (zp + row)[r];
       }
     }
+    const bool inside = kb * 128 + 128 <= p.K;
+    const int k = kb * 128 + xcol * 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = kb * 128 + j * 32 + c * 8;
+    for (int i = 0; i < R; ++i) {
+      if constexpr (WIDE) {
+        const uint32_t off = inside || k < p.K ? xo[i] : kOOB;
+        xq[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off, kb * 256, 0));
+      } else {
+        const uint16_t* row = xb + (int64_t)(4 * i + xrow) * p.ldx;
+        const bool row_in = m0 + 4 * i + xrow < p.M;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if constexpr (WIDE) {
-          const uint32_t off = k < p.K ? xo[m] + (uint32_t)k * 2 : kOOB;
-          xq[u][j][m] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off | (xo[m] & kOOB), 0, 0));
-        } else {
-          const uint16_t* row = xb + (int64_t)(m * 16 + r) * p.ldx;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool row_in = m0 + m * 16 + r < p.M;
-            const uint32_t lo = row_in && k + 2 * i < p.K ? row[k + 2 * i] : 0;
-            const uint32_t hi = row_in && k + 2 * i + 1 < p.K ? row[k + 2 * i + 1] : 0;
-            xq[u][j][m][i] = lo | hi << 16;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = row_in && k + 2 * e < p.K ? row[k + 2 * e] : 0;
+          const uint32_t hi = row_in && k + 2 * e + 1 < p.K ? row[k + 2 * e + 1] : 0;
+          xq[u][i][e] = lo | hi << 16;
         }
       }
     }
@@ -119,63 +149,82 @@ __global__ __launch_bounds__(512) void w4_kernel(W4Args p) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t) total[m][t] = f32x4{0, 0, 0, 0};
+  uint32_t expo = BF16 ? 0x41804180u : 0x4c004c00u;
+  asm("" : "+v"(expo));
   const u32x4 ones = BF16 ? u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}
                           : u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 
 #pragma unroll
-  for (int u = 0; u < U; ++u) load(u, wave + u * W);
-  for (int base = wave; base < KB; base += U * W) {
+  for (int u = 0; u < U; ++u) load(u, kw + u * KW);
+  for (int base = kw; base < KB; base += U * KW) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (base + u * W >= KB) break;
+      if (base + u * KW >= KB) break;
+#pragma unroll
+      for (int i = 0; i < R; ++i) xs[(4 * i + xrow) * 16 + (xcol ^ ((4 * i + xrow) & 15))] = xq[u][i];
+      u32x4 xf[4][MT];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xf[j][m] = xs[(16 * m + r) * 16 + ((4 * j + c) ^ r)];
+      u32x4 w[NT];
+      float sc[FL][NT], of[FL][NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        w[t] = wq[u][t];
+#pragma unroll
+        for (int f = 0; f < FL; ++f) {
+          sc[f][t] = from16<BF16>(sq[u][f][t]);
+          of[f][t] = has_z ? -16.f - (float)zq[u][f][t] : -24.f;
+        }
+      }
+      load(u, base + (u + U) * KW);
 #pragma unroll
       for (int f = 0; f < FL; ++f) {
-        f32x4 rs[MT], ps[MT][NT];
+        f32x4 rs[MT];
+        const f32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int j = f * PER + i;
-          const f32x4 zero = {0, 0, 0, 0};
+        for (int i = 0; i < PER; ++i)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) rs[m] = mma<BF16>(xq[u][j][m], ones, i ? rs[m] : zero);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const u32x4 b = unpack<BF16>(wq[u][t][j]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) ps[m][t] = mma<BF16>(xq[u][j][m], b, i ? ps[m][t] : zero);
-          }
-        }
+          for (int m = 0; m < MT; ++m) rs[m] = mma<BF16>(xf[f * PER + i][m], ones, i ? rs[m] : zero);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float s = from16<BF16>(sq[u][f][t]), z = -16.f - (float)zq[u][f][t];
+          f32x4 ps[MT];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const u32x4 b = unpack<BF16>(w[t][f * PER + i], expo);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) ps[m] = mma<BF16>(xf[f * PER + i][m], b, i ? ps[m] : zero);
+          }
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) total[m][t][e] += s * __builtin_fmaf(z, rs[m][e], ps[m][t][e]);
+            for (int e = 0; e < 4; ++e) total[m][t][e] = __builtin_fmaf(sc[f][t], __builtin_fmaf(of[f][t], rs[m][e], ps[m][e]), total[m][t][e]);
         }
       }
-      load(u, base + (u + U) * W);
     }
   }
 
-  // red[wave][m][t][lane] as 4 tokens each; summed in wave order
+  // red[kw][mw][m][t][lane] as 4 tokens each; summed in the order of kw
   constexpr int PART = MT * NT * 64;
   f32x4* part = reinterpret_cast<f32x4*>(red);
+  __syncthreads();  // every wave is done with its piece
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t) part[wave * PART + (m * NT + t) * 64 + lane] = total[m][t];
   __syncthreads();
-  // thread -> (m, t, l): lanes of 16 neighbours hold 16 neighbouring columns of four tokens
-  for (int i = threadIdx.x; i < PART; i += blockDim.x) {
+  // thread -> (mw, m, t, l): lanes of 16 neighbours hold 16 neighbouring columns of four tokens
+  for (int i = threadIdx.x; i < MW * PART; i += blockDim.x) {
     f32x4 y = part[i];
-    for (int w = 1; w < W; ++w) y += part[w * PART + i];
-    const int l = i & 63, t = (i >> 6) % NT, m = (i >> 6) / NT;
+    for (int w = 1; w < KW; ++w) y += part[w * MW * PART + i];
+    const int l = i & 63, t = (i >> 6) % NT, m = (i >> 6) / NT;  // m counts over the MW waves' tiles
     const int n = (nb0 + t) * 16 + (l & 15);
     if (n >= p.N) continue;
     const float b = p.bias ? from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]) : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int row = m0 + m * 16 + (l >> 4) * 4 + e;
+      const int row = blockIdx.y * (16 * MT * MW) + m * 16 + (l >> 4) * 4 + e;
       if (row < p.M) static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(y[e] + b);
     }
   }
@@ -190,22 +239,43 @@ __global__ __launch_bounds__(256) void w4_bias_kernel(W4Args p) {
   static_cast<uint16_t*>(p.y)[i / p.N * p.ldy + n] = p.bias ? static_cast<const uint16_t*>(p.bias)[n] : (uint16_t)0;
 }
 
-template <bool BF16, int MT, int NT, int U, int PER, bool WIDE>
+// WMAX: the waves of one workgroup, and of all workgroups on a compute unit,
+// that the instance's registers allow.  K is split over as many waves as let
+// all workgroups run at once.
+template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX, bool WIDE>
 hipError_t run(const W4Args& a, hipStream_t s) {
+  static_assert(NT <= 4 && WMAX * MT * 4096 <= 160 << 10, "the sums lie where x was");
   const int NB = (a.N + 15) / 16, KB = (a.K + 127) / 128;
-  const int W = KB < 8 ? KB : 8;
-  const dim3 grid((NB + NT - 1) / NT, (a.M + 16 * MT - 1) / (16 * MT));
+  const dim3 grid((NB + NT - 1) / NT, (a.M + 16 * MT * MW - 1) / (16 * MT * MW));
   if (grid.y > 65535) return hipErrorInvalidConfiguration;
-  w4_kernel<BF16, MT, NT, U, PER, WIDE><<<grid, 64 * W, W * MT * NT * 1024, s>>>(a);
+  const int64_t each = ((int64_t)grid.x * grid.y + a.cus - 1) / a.cus;
+  int kw = each < WMAX / MW ? WMAX / MW / (int)each : 1;
+  if (kw < 4 / MW) kw = 4 / MW;
+  if (kw > KB) kw = KB;
+  w4_kernel<BF16, MT, NT, U, PER, R, MW, WMAX, WIDE><<<grid, 64 * kw * MW, kw * MW * MT * 4096, s>>>(a);
   return hipGetLastError();
+}
+
+template <bool BF16, int PER, int R>
+hipError_t few(const W4Args& a, hipStream_t s) {
+  const int NB = (a.N + 15) / 16;
+  if (NB < 1024) return run<BF16, 1, 1, 2, PER, R, 1, 16, true>(a, s);
+  return run<BF16, 1, 2, 2, PER, R, 1, R == 4 || PER == 1 ? 12 : 16, true>(a, s);
 }
 
 template <bool BF16, int PER>
 hipError_t wide(const W4Args& a, hipStream_t s) {
-  if (a.M <= 8) return run<BF16, 1, 1, 4, PER, true>(a, s);
-  if (a.M <= 16) return run<BF16, 1, 2, 4, PER, true>(a, s);
-  if (a.M <= 32) return run<BF16, 2, 2, 2, PER, true>(a, s);
-  return run<BF16, 4, 4, 1, PER, true>(a, s);
+  const int NB = (a.N + 15) / 16;
+  if (a.M <= 4) return few<BF16, PER, 1>(a, s);
+  if (a.M <= 8) return few<BF16, PER, 2>(a, s);
+  if (a.M <= 16) return few<BF16, PER, 4>(a, s);
+  if (a.M <= 32) {
+    if (NB < 512) return run<BF16, 2, 1, 1, PER, 8, 1, 16, true>(a, s);
+    return run<BF16, 2, 2, 1, PER, 8, 1, PER == 1 ? 8 : 12, true>(a, s);
+  }
+  if (NB < 512) return run<BF16, 2, 1, 1, PER, 8, 2, 16, true>(a, s);
+  if constexpr (PER == 4) return run<BF16, 2, 4, 1, PER, 8, 2, 12, true>(a, s);
+  else return run<BF16, 2, 2, 1, PER, 8, 2, PER == 1 ? 8 : 12, true>(a, s);
 }
 
 template <bool BF16>
@@ -218,7 +288,7 @@ hipError_t pick(const W4Args& a, hipStream_t s) {
   }
   // 16-byte rows, and tile rows that a 31-bit byte offset reaches
   if ((reinterpret_cast<uintptr_t>(a.x) & 15) || a.ldx % 8 || a.K % 8 || a.ldx > (1 << 23) || a.K > (1 << 23))
-    return run<BF16, 1, 1, 1, 1, false>(a, s);
+    return run<BF16, 1, 1, 1, 1, 4, 1, 8, false>(a, s);
   if (a.group % 128 == 0) return wide<BF16, 4>(a, s);
   if (a.group % 64 == 0 && 128 % a.group == 0) return wide<BF16, 2>(a, s);
   return wide<BF16, 1>(a, s);
