@@ -57,7 +57,7 @@ DEVICE = ["--offload-arch=" + ARCH,
 
 # Attention rescales its accumulators between matrix products: with those in
 # ordinary registers there are no copies out of and into accumulator registers.
-EXTRA = {"attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in ("attend.hip", "attend_tile.hip")}
 
 
 def _compile_cmds(folder=CSRC, prefix=""):

@@ -24,7 +24,7 @@
 // byte in a 16-bit slot, less 128 2^-24 (packed, exact).  Leaving the offset to
 // the sums instead saves that subtraction, but costs the small results of a
 // sum whose large terms are zero: 128 of them take the place of its low bits.
-#include "device.hpp"
+#include "attend.hpp"
 
 namespace mid {
 namespace {
@@ -32,118 +32,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;
 constexpr int kItem = 16;  // what starting and ending an item costs, in tiles
-constexpr int kRsrcWord3 = 0x00020000;
-constexpr int kDeviceScope = 16;  // cache policy SC1
-constexpr float kTiny = 0x1p-24f;  // int8 codes as operands are in units of this
-
-__device__ inline f32x4 mma(h8 a, h8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-
-// over the lanes that share lane % 16
-template <typename F>
-__device__ inline float join16(float x, F f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, x);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const uint32_t a0 = a[0], a1 = a[1];
-  const uint32_t w = __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1)));
-  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  const uint32_t b0 = b[0], b1 = b[1];
-  return f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
-}
-__device__ inline float max16(float x) { return join16(x, [](float a, float b) { return fmaxf(a, b); }); }
-__device__ inline float sum16(float x) { return join16(x, [](float a, float b) { return a + b; }); }
-__device__ inline int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
-__device__ inline float lane_value(float x, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
-}
-
-// Two bytes code + 128 in 16-bit slots as two numbers code 2^-24.
-__device__ inline uint32_t centred(uint32_t w) {
-  const _Float16 off = (_Float16)(-128.f * kTiny);
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, w) + h2{off, off});
-}
-
-// Eight codes of one token as eight numbers, in order.
-template <int CODE>
-__device__ inline h8 along(uint32_t w0, uint32_t w1) {
-  u32x4 o;
-  if constexpr (CODE == MI_DECODE_INT8) {
-    w0 ^= 0x80808080u, w1 ^= 0x80808080u;
-    o[0] = centred(__builtin_amdgcn_perm(0u, w0, 0x0c010c00u));
-    o[1] = centred(__builtin_amdgcn_perm(0u, w0, 0x0c030c02u));
-    o[2] = centred(__builtin_amdgcn_perm(0u, w1, 0x0c010c00u));
-    o[3] = centred(__builtin_amdgcn_perm(0u, w1, 0x0c030c02u));
-  } else {
-    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false));
-    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true));
-    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false));
-    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true));
-  }
-  return __builtin_bit_cast(h8, o);
-}
-
-// Channels 2 B and 2 B + 1 of eight tokens' words as eight numbers each, in token order.
-template <int CODE, int B>
-__device__ inline void across(const uint32_t (&w)[8], h8& even, h8& odd) {
-  u32x4 e, o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t t0 = w[2 * i], t1 = w[2 * i + 1];
-    if constexpr (CODE == MI_DECODE_INT8) {
-      e[i] = centred(__builtin_amdgcn_perm(t1, t0, 0x0c040c00u + 0x00020002u * B));
-      o[i] = centred(__builtin_amdgcn_perm(t1, t0, 0x0c050c01u + 0x00020002u * B));
-    } else {
-      const uint32_t y = __builtin_amdgcn_perm(t1, t0, 0x05010400u + 0x02020202u * B);
-      e[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.f, false));
-      o[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(y, 1.f, true));
-    }
-  }
-  even = __builtin_bit_cast(h8, e);
-  odd = __builtin_bit_cast(h8, o);
-}
-
-// One row block of one sequence.
-struct Block {
-  int first, rows;  // the sequence's first token, the block's rows
-  int r0;           // the block's first row
-  int start;        // position of the sequence's first query token
-  int plo, phi;     // positions of the block's first and last row
-  int ns, lo;       // tiles of sinks, and the first tile after them
-  int tiles;        // 0: no rows
-  int b;            // the sequence
-  __device__ int token(int t) const { return kTile * (t < ns ? t : lo + t - ns); }
-  __device__ Block of_lane(int l) const {
-    Block k;
-    k.first = __builtin_amdgcn_readlane(first, l), k.rows = __builtin_amdgcn_readlane(rows, l);
-    k.r0 = __builtin_amdgcn_readlane(r0, l), k.start = __builtin_amdgcn_readlane(start, l);
-    k.plo = __builtin_amdgcn_readlane(plo, l), k.phi = __builtin_amdgcn_readlane(phi, l);
-    k.ns = __builtin_amdgcn_readlane(ns, l), k.lo = __builtin_amdgcn_readlane(lo, l);
-    k.tiles = __builtin_amdgcn_readlane(tiles, l), k.b = __builtin_amdgcn_readlane(b, l);
-    return k;
-  }
-};
-__device__ inline Block block_of(const AttendArgs& p, int G, int block_rows, int blocks, int pair, int pairs) {
-  Block k = {};
-  if (pair >= pairs) return k;
-  const int b = blocks == 1 ? pair : pair / blocks, rb = pair - b * blocks;
-  k.b = b;
-  const Span sp = span_of(p.batch, b);
-  const int64_t cap = (int64_t)p.batch.table_cols * p.cache.page_size;
-  const int len = (int)min((int64_t)max(p.batch.lens[b], 0), cap);
-  k.first = sp.first;
-  k.r0 = rb * block_rows;
-  const int64_t all = (int64_t)min(sp.n, p.batch.max_tokens) * G;
-  k.rows = (int)min((int64_t)block_rows, all - k.r0);
-  k.start = len - sp.n;
-  k.plo = k.start + k.r0 / G;
-  k.phi = k.start + (k.r0 + k.rows - 1) / G;
-  if (p.window) {
-    const int lo = max(0, k.plo - p.window + 1);
-    k.lo = lo / kTile;
-    k.ns = min((int)(((int64_t)min(p.sinks, max(k.phi + 1, 0)) + kTile - 1) / kTile), k.lo);
-  }
-  k.tiles = k.rows <= 0 ? 0 : max(1, k.ns + max(k.phi, 0) / kTile + 1 - k.lo);
-  return k;
-}
 
 template <int CODE, int D, int NT>
 __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_kernel(AttendArgs p, int blocks) {
@@ -157,13 +45,13 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
   const int lane = threadIdx.x & 63, tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int H = p.cache.kv_heads, G = p.q_heads / H, ps = p.cache.page_size;
+  const int H = p.cache.kv_heads, G = p.q_heads / H, ps = p.cache.page_size, log_ps = __builtin_ctz((unsigned)ps);
   const int pairs = p.batch.batch * blocks;
 
   // the line's length, and where this workgroup's piece begins; lane i knows
   // row block `at` + i, and the wave takes its numbers from there
   int at = 0;
-  Block mine = block_of(p, G, ROWS, blocks, lane, pairs);
+  Block<kTile> mine = block_of<kTile>(p, G, ROWS, blocks, lane, pairs);
   int64_t total = 0;
   uint32_t ahead = 0;  // line of the blocks up to the lane's own, for one head
   auto extend = [&]() {
@@ -179,7 +67,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     total += extend();
     if (at + 64 >= pairs) break;
     at += 64;
-    mine = block_of(p, G, ROWS, blocks, at + lane, pairs);
+    mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
   }
   total *= H;
   const int64_t each = (int64_t)((double)total / (double)(int)gridDim.x) + 1;
@@ -190,7 +78,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
   if (at > 0) {
     at = 0;
     while (true) {
-      mine = block_of(p, G, ROWS, blocks, at + lane, pairs);
+      mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
       const uint32_t more = extend();
       if ((before + more) * H > begin) break;
       before += more;
@@ -198,7 +86,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     }
   }
   int who = __builtin_ctzll(__ballot((before + ahead) * H > begin));  // the block's lane
-  Block blk = mine.of_lane(who);
+  Block<kTile> blk = mine.of_lane(who);
   int h, v0;  // head, and where in the item's line the piece begins
   {
     const uint32_t off = (uint32_t)(begin - (before + (uint32_t)lane_value((int)ahead, who) - (blk.tiles + kItem)) * H);
@@ -208,10 +96,10 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
   int64_t left = end - begin;
 
   // a part: sums of ROWS x D, then m and l of each row
-  constexpr uint32_t kPart = 4 * ROWS * (D + 2);
+  constexpr uint32_t kPart = part_bytes<ROWS, D>();
   const auto parts_at = __builtin_amdgcn_make_buffer_rsrc(p.ws, (short)0, (int)MI_DECODE_WORKSPACE_BYTES, kRsrcWord3);
 
-  auto item = [&](const Block& blk, int h, int s0, int s1) {
+  auto item = [&](const Block<kTile>& blk, int h, int s0, int s1) {
     const int32_t* table = p.batch.table + (int64_t)blk.b * p.batch.table_stride;
 
     // the block's queries: rows as columns of the right operand.  Of several
@@ -240,7 +128,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
         const bool some = t < s1 && tok <= blk.phi &&
                           (p.window == 0 || tok + 15 > blk.plo - p.window || tok < p.sinks);
         pg[st] = -1;
-        if (some) pg[st] = table[tok / ps];
+        if (some) pg[st] = table[tok >> log_ps];
       }
 #pragma unroll
       for (int st = 0; st < 2; ++st)
@@ -311,9 +199,6 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
         }
       }
     };
-    auto seen = [&](int tok, int at) {
-      return tok <= at && (p.window == 0 || tok > at - p.window || tok < p.sinks);
-    };
     int tile = s0 + wave, i = 0;
     pages(tile);
     scales();
@@ -379,6 +264,13 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       float vr0 = lane_value(vr[0], i), vr1 = lane_value(vr[1], i);
       const bool whole = pg0 >= 0 && pg1 >= 0 && tok0 + kTile - 1 <= blk.plo &&
                          (p.window == 0 || tok0 > blk.phi - p.window || tok0 + kTile - 1 < p.sinks);
+      // whether a query at `at` sees the lane's token c: constants against
+      // numbers of the tile, which otherwise stay in registers as tokens
+      const int from = tok0 + 4 * g;
+      auto seen = [&](int c, int at) {
+        const int upto = at - from;
+        return c <= upto && (p.window == 0 || c > upto - p.window || c < p.sinks - from);
+      };
       const int next = tile + kWaves;
       if (++i == 64) {
         i = 0;
@@ -427,7 +319,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
           for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if ((st ? pg1 : pg0) < 0 || !seen(tok0 + 16 * st + 4 * g + e, pos[nt])) z[nt][st][e] = -INFINITY;
+              if ((st ? pg1 : pg0) < 0 || !seen(16 * st + e, pos[nt])) z[nt][st][e] = -INFINITY;
         }
         float top = fmaxf(fmaxf(fmaxf(z[nt][0][0], z[nt][0][1]), fmaxf(z[nt][0][2], z[nt][0][3])),
                           fmaxf(fmaxf(z[nt][1][0], z[nt][1][1]), fmaxf(z[nt][1][2], z[nt][1][3])));
@@ -474,7 +366,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
               if (mine) vraw[e][x] = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              if (mine && seen(tok, pos[nt])) pf[nt][e] = (_Float16)NAN;
+              if (mine && seen(16 * (e / 4) + e % 4, pos[nt])) pf[nt][e] = (_Float16)NAN;
           }
         }
       }
@@ -499,18 +391,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       load_v(i, next);
     }
 
-    auto store = [&](int rr, int d, f32x4 x, float sum) {
-      const int r = blk.r0 + rr;
-      uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
-                      (h * G + r % G) * p.out.head_stride + d;
-      u32x2 y = {0, 0};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v = sum == 0.f ? 0.f : x[k] / sum;
-        y[k / 2] |= (uint32_t)(p.bf16 ? to16<true>(v) : to16<false>(v)) << (16 * (k % 2));
-      }
-      *reinterpret_cast<u32x2*>(out) = y;
-    };
+    auto store = [&](int rr, int d, f32x4 x, float sum) { store_row(p, blk, h, G, rr, d, x, sum); };
 
     // the four waves' sums to one
 #pragma unroll
@@ -566,77 +447,10 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     if (!whole_item) {
       const int earlier = (s0 + chunk - 1) / chunk, later = (blk.tiles - s1 + chunk - 1) / chunk;
       const int first = (int)blockIdx.x - earlier, parts = earlier + 1 + later;
-      // Workgroups of one item run on XCDs whose L2 caches are not coherent.
-      // Parts are stored and loaded with device scope, past those caches, and
-      // counted when their stores are acknowledged; fences would write back
-      // and drop whole caches instead (15 to 25 us between the two stores).
-      __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xf << 8));  // vmcnt(0)
-      __syncthreads();
-      if (tid == 0) last_flag = __hip_atomic_fetch_add(p.cnt + first, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
-      __syncthreads();
-      if (last_flag) {
+      const bool last = last_to_arrive(p.cnt + first, parts, &last_flag);
+      if (last) {
         auto part = [&](int n) { return (uint32_t)(2 * (first + n) + (n == 0)) * kPart; };
-        // A thread adds four channels of a row over every groups-th part; where
-        // there are few rows, groups of threads share the parts.  Loads of
-        // several parts are in flight at a time: one after the other, a part
-        // costs the memory's latency (32 parts of 4 rows: 45 us).
-        const int all = blk.rows * (D / 4);
-        int groups = 1;
-        while (groups < 8 && 2 * groups * all <= 64 * kWaves && 2 * groups <= parts) groups *= 2;
-        const int per = 64 * kWaves / groups, grp = tid / per;
-        for (int e = tid % per; e < all; e += per) {
-          const int rr = e / (D / 4), d = e % (D / 4) * 4;
-          float top = -INFINITY, sum = 0.f;
-          f32x4 x = {0, 0, 0, 0};
-          for (int n = grp; n < parts; n += 8 * groups) {
-            float pm[8], pl[8];
-            f32x4 px[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t s = part(min(n + k * groups, parts - 1));
-              const f32x2 ml = __builtin_bit_cast(
-                  f32x2, __builtin_amdgcn_raw_buffer_load_b64(parts_at, s + 4 * (ROWS * D + 2 * rr), 0, kDeviceScope));
-              pm[k] = ml[0], pl[k] = ml[1];
-              px[k] = __builtin_bit_cast(
-                  f32x4, __builtin_amdgcn_raw_buffer_load_b128(parts_at, s + 4 * (rr * D + d), 0, kDeviceScope));
-            }
-            float t1 = top;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) t1 = fmaxf(t1, pm[k]);
-            const float base = t1 == -INFINITY ? 0.f : t1, down = __builtin_amdgcn_exp2f(top - base);
-            top = t1, x *= down, sum *= down;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (n + k * groups >= parts) break;
-              const float f = __builtin_amdgcn_exp2f(pm[k] - base);
-              sum += f * pl[k];
-              x += f * px[k];
-            }
-          }
-          if (groups > 1) {  // then every thread has one element at most
-            float* mine = &obuf[0][0][0] + 6 * tid;
-            mine[0] = top, mine[1] = sum;
-            mine[2] = x[0], mine[3] = x[1], mine[4] = x[2], mine[5] = x[3];
-          } else {
-            store(rr, d, x, sum);
-          }
-        }
-        if (groups > 1) {
-          __syncthreads();
-          for (int e = tid; e < all; e += 64 * kWaves) {
-            float top = -INFINITY, sum = 0.f;
-            f32x4 x = {0, 0, 0, 0};
-            for (int k = 0; k < groups; ++k) top = fmaxf(top, (&obuf[0][0][0])[6 * (k * per + e)]);
-            const float base = top == -INFINITY ? 0.f : top;
-            for (int k = 0; k < groups; ++k) {
-              const float* s = &obuf[0][0][0] + 6 * (k * per + e);
-              const float f = __builtin_amdgcn_exp2f(s[0] - base);
-              sum += f * s[1];
-              x += f * f32x4{s[2], s[3], s[4], s[5]};
-            }
-            store(e / (D / 4), e % (D / 4) * 4, x, sum);
-          }
-        }
+        join_parts<kTile, ROWS, D, 64 * kWaves>(p, parts_at, blk, h, G, parts, part, &obuf[0][0][0]);
         if (tid == 0) __hip_atomic_store(p.cnt + first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
@@ -655,7 +469,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     do {
       if (++who == 64) {
         who = 0, at += 64;
-        mine = block_of(p, G, ROWS, blocks, at + lane, pairs);
+        mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
       }
       blk = mine.of_lane(who);
     } while (blk.tiles == 0);
@@ -699,6 +513,8 @@ hipError_t dims_of(const AttendArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
+  if (rows > 64) return launch_attend_tile(a, s);
   return a.cache.code == MI_DECODE_INT8 ? dims_of<MI_DECODE_INT8>(a, s) : dims_of<MI_DECODE_E4M3>(a, s);
 }
 

@@ -309,8 +309,10 @@ mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cac
   a.out = *out;
   a.max_len = max_len;
   a.q_heads = q_heads;
-  a.window = window;
-  a.sinks = sinks;
+  // positions are below 2^30: a longer window hides nothing, and the kernels'
+  // differences of positions and these stay within 32 bits
+  a.window = window < (1 << 30) ? window : 0;
+  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   a.scale = scale;
   a.ws = h->ws;
   a.cnt = h->cnt;

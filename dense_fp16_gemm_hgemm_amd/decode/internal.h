@@ -53,7 +53,8 @@ struct AttendArgs : KvArgs {
 hipError_t launch_w4(const W4Args& a, hipStream_t s);
 hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 hipError_t launch_read(const ReadArgs& a, hipStream_t s);
-hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
+hipError_t launch_attend(const AttendArgs& a, hipStream_t s);       // any number of rows
+hipError_t launch_attend_tile(const AttendArgs& a, hipStream_t s);  // many rows a sequence
 
 constexpr int kCounters = 65536;
 
