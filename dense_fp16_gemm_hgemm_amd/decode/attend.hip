@@ -31,6 +31,9 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;
+// Parts of an item, in bytes, up to which its last workgroup adds them itself;
+// beyond, a second kernel does.
+constexpr int64_t kJoinInside = 192 << 10;
 constexpr int kItem = 16;  // what starting and ending an item costs, in tiles
 
 template <int CODE, int D, int NT>
@@ -73,6 +76,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
   const int64_t each = (int64_t)((double)total / (double)(int)gridDim.x) + 1;
   const int chunk = (int)((each + kWaves - 1) / kWaves) * kWaves;
   const int64_t begin = (int64_t)blockIdx.x * chunk, end = min(begin + chunk, total);
+  if (p.join && tid == 0) p.join[blockIdx.x].parts = 0;
   if (begin >= end) return;
   int64_t before = 0;
   if (at > 0) {
@@ -96,7 +100,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
   int64_t left = end - begin;
 
   // a part: sums of ROWS x D, then m and l of each row
-  constexpr uint32_t kPart = part_bytes<ROWS, D>();
+  constexpr uint32_t kPart = part_bytes(ROWS, D);
   const auto parts_at = __builtin_amdgcn_make_buffer_rsrc(p.ws, (short)0, (int)MI_DECODE_WORKSPACE_BYTES, kRsrcWord3);
 
   auto item = [&](const Block<kTile>& blk, int h, int s0, int s1) {
@@ -391,7 +395,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
       load_v(i, next);
     }
 
-    auto store = [&](int rr, int d, f32x4 x, float sum) { store_row(p, blk, h, G, rr, d, x, sum); };
+    auto store = [&](int rr, int d, f32x4 x, float sum) { store_row(p, blk.first, blk.r0 + rr, h, G, d, x, sum); };
 
     // the four waves' sums to one
 #pragma unroll
@@ -447,14 +451,15 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     if (!whole_item) {
       const int earlier = (s0 + chunk - 1) / chunk, later = (blk.tiles - s1 + chunk - 1) / chunk;
       const int first = (int)blockIdx.x - earlier, parts = earlier + 1 + later;
-      const bool last = last_to_arrive(p.cnt + first, parts, &last_flag);
-      if (last) {
-        auto part = [&](int n) { return (uint32_t)(2 * (first + n) + (n == 0)) * kPart; };
-        join_parts<kTile, ROWS, D, 64 * kWaves>(p, parts_at, blk, h, G, parts, part, &obuf[0][0][0]);
+      const JoinItem it = {blk.first, blk.r0, blk.rows, h, parts, (uint32_t)(2 * first + 1) * kPart,
+                           (uint32_t)(2 * first + 2) * kPart, 2 * kPart};
+      if (p.join) {
+        if (s0 == 0 && tid == 0) p.join[blockIdx.x] = it;  // one item that goes on in other workgroups
+      } else if (last_to_arrive(p.cnt + first, parts, &last_flag)) {
+        join_parts<D, 64 * kWaves, 16>(p, parts_at, it, ROWS, 0, blk.rows, &obuf[0][0][0]);
         if (tid == 0) __hip_atomic_store(p.cnt + first, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
-
   };
 
   while (true) {
@@ -462,7 +467,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_ker
     const int s0 = max(v0 - kItem, 0), s1 = max(v1 - kItem, 0);
     if (s1 > s0) item(blk, h, s0, s1);
     left -= v1 - v0;
-    if (left <= 0) return;
+    if (left <= 0) break;
     v0 = 0;
     if (++h < H) continue;
     h = 0;
@@ -486,8 +491,13 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   static_assert(sizeof(float) * ROWS * (D + 2) * 2 * 2 * 304 <= MI_DECODE_WORKSPACE_BYTES, "partial results");
   const double tiles = (double)blocks * a.batch.batch * a.cache.kv_heads * (a.max_len / kTile + 1);
   if (tiles < grid) grid = (int)tiles;
-  attend_kernel<CODE, D, NT><<<grid, 64 * kWaves, 0, s>>>(a, (int)blocks);
-  return hipGetLastError();
+  // an item has grid / kv_heads parts at most: a sequence's heads are alike
+  const int64_t part_rows = (grid / a.cache.kv_heads + 1) * (rows < ROWS ? rows : ROWS);
+  AttendArgs b = a;
+  if (part_rows * D * 4 <= kJoinInside) b.join = nullptr;
+  attend_kernel<CODE, D, NT><<<grid, 64 * kWaves, 0, s>>>(b, (int)blocks);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || !b.join ? e : launch_join(b, grid, ROWS, s);
 }
 
 template <int CODE, int D>
@@ -514,7 +524,10 @@ hipError_t dims_of(const AttendArgs& a, hipStream_t s) {
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
-  if (rows > 64) return launch_attend_tile(a, s);
+  // us, here and there, 32 x 8 items against 4096 tokens: 64 rows of 128 channels
+  // 117 and 162, 80 rows 204 and 166; 512 rows of 256 channels 1408 and 1317,
+  // 256 rows (1 x 8 items, 8192 tokens) 62 and 70
+  if (rows > (a.cache.head_dim == 256 ? 511 : 64)) return launch_attend_tile(a, s);
   return a.cache.code == MI_DECODE_INT8 ? dims_of<MI_DECODE_INT8>(a, s) : dims_of<MI_DECODE_E4M3>(a, s);
 }
 

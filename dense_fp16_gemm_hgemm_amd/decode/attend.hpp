@@ -124,11 +124,10 @@ __device__ inline Block<TILE> block_of(const AttendArgs& p, int G, int block_row
   return k;
 }
 
-// Four channels of a row's result.
-template <int TILE>
-__device__ inline void store_row(const AttendArgs& p, const Block<TILE>& blk, int h, int G, int rr, int d, f32x4 x, float sum) {
-  const int r = blk.r0 + rr;
-  uint16_t* out = static_cast<uint16_t*>(p.out.data) + (blk.first + r / G) * p.out.token_stride +
+// Four channels of a row's result: row r of the sequence whose first token is
+// `first`, key-value head h.
+__device__ inline void store_row(const AttendArgs& p, int first, int r, int h, int G, int d, f32x4 x, float sum) {
+  uint16_t* out = static_cast<uint16_t*>(p.out.data) + (first + r / G) * p.out.token_stride +
                   (h * G + r % G) * p.out.head_stride + d;
   u32x2 y = {0, 0};
 #pragma unroll
@@ -140,8 +139,7 @@ __device__ inline void store_row(const AttendArgs& p, const Block<TILE>& blk, in
 }
 
 // A part in the workspace: sums of ROWS x D, then m and l of each row.
-template <int ROWS, int D>
-constexpr uint32_t part_bytes() { return 4 * ROWS * (D + 2); }
+constexpr uint32_t part_bytes(int rows, int D) { return 4 * (uint32_t)rows * (D + 2); }
 
 // Counts a workgroup in whose part is stored; true in the last of `parts`.
 //
@@ -157,43 +155,47 @@ __device__ inline bool last_to_arrive(int* cnt, int parts, int* flag) {
   return *flag;
 }
 
-// Adds a row block's parts in order and stores the result; part(n) is where
-// part n lies, smem room for 6 THREADS floats.
-template <int TILE, int ROWS, int D, int THREADS, typename Rsrc, typename Part>
-__device__ inline void join_parts(const AttendArgs& p, const Rsrc& parts_at, const Block<TILE>& blk, int h, int G,
-                                  int parts, Part part, float* smem) {
-  const int tid = threadIdx.x;
-  // A thread adds four channels of a row over every groups-th part; where
-  // there are few rows, groups of threads share the parts.  Loads of
-  // several parts are in flight at a time: one after the other, a part
-  // costs the memory's latency (32 parts of 4 rows: 45 us).
-  const int all = blk.rows * (D / 4);
+// A row block in parts: part 0 lies at `head`, part n at `tail` + (n - 1) `step`.
+__device__ inline uint32_t part_at(const JoinItem& it, int n) { return n == 0 ? it.head : it.tail + (uint32_t)(n - 1) * it.step; }
+
+// Adds the parts of rows r0 .. r0 + rows - 1 of a block in order and stores the
+// result; smem: room for 6 THREADS floats.
+//
+// A thread adds four channels of a row over every groups-th part; where there
+// are few rows, groups of threads share the parts.  DEPTH parts' loads are in
+// flight at a time: one after the other, a part costs the memory's latency (32
+// parts of 4 rows: 45 us).
+template <int D, int THREADS, int DEPTH, typename Rsrc>
+__device__ inline void join_parts(const AttendArgs& p, const Rsrc& parts_rsrc, const JoinItem& it, int block_rows,
+                                  int r0, int rows, float* smem) {
+  const int tid = threadIdx.x, G = p.q_heads / p.cache.kv_heads, parts = it.parts;
+  const int all = rows * (D / 4);
   int groups = 1;
   while (groups < 8 && 2 * groups * all <= THREADS && 2 * groups <= parts) groups *= 2;
   const int per = THREADS / groups, grp = tid / per;
   for (int e = tid % per; e < all; e += per) {
-    const int rr = e / (D / 4), d = e % (D / 4) * 4;
+    const int rr = r0 + e / (D / 4), d = e % (D / 4) * 4;
     float top = -INFINITY, sum = 0.f;
     f32x4 x = {0, 0, 0, 0};
-    for (int n = grp; n < parts; n += 8 * groups) {
-      float pm[8], pl[8];
-      f32x4 px[8];
+    for (int n = grp; n < parts; n += DEPTH * groups) {
+      float pm[DEPTH], pl[DEPTH];
+      f32x4 px[DEPTH];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t s = part(min(n + k * groups, parts - 1));
+      for (int k = 0; k < DEPTH; ++k) {
+        const uint32_t s = part_at(it, min(n + k * groups, parts - 1));
         const f32x2 ml = __builtin_bit_cast(
-            f32x2, __builtin_amdgcn_raw_buffer_load_b64(parts_at, s + 4 * (ROWS * D + 2 * rr), 0, kDeviceScope));
+            f32x2, __builtin_amdgcn_raw_buffer_load_b64(parts_rsrc, s + 4 * (block_rows * D + 2 * rr), 0, kDeviceScope));
         pm[k] = ml[0], pl[k] = ml[1];
         px[k] = __builtin_bit_cast(
-            f32x4, __builtin_amdgcn_raw_buffer_load_b128(parts_at, s + 4 * (rr * D + d), 0, kDeviceScope));
+            f32x4, __builtin_amdgcn_raw_buffer_load_b128(parts_rsrc, s + 4 * (rr * D + d), 0, kDeviceScope));
       }
       float t1 = top;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) t1 = fmaxf(t1, pm[k]);
+      for (int k = 0; k < DEPTH; ++k) t1 = fmaxf(t1, pm[k]);
       const float base = t1 == -INFINITY ? 0.f : t1, down = __builtin_amdgcn_exp2f(top - base);
       top = t1, x *= down, sum *= down;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < DEPTH; ++k) {
         if (n + k * groups >= parts) break;
         const float f = __builtin_amdgcn_exp2f(pm[k] - base);
         sum += f * pl[k];
@@ -205,7 +207,7 @@ __device__ inline void join_parts(const AttendArgs& p, const Rsrc& parts_at, con
       mine[0] = top, mine[1] = sum;
       mine[2] = x[0], mine[3] = x[1], mine[4] = x[2], mine[5] = x[3];
     } else {
-      store_row(p, blk, h, G, rr, d, x, sum);
+      store_row(p, it.first, it.r0 + rr, it.h, G, d, x, sum);
     }
   }
   if (groups > 1) {
@@ -221,7 +223,7 @@ __device__ inline void join_parts(const AttendArgs& p, const Rsrc& parts_at, con
         sum += f * s[1];
         x += f * f32x4{s[2], s[3], s[4], s[5]};
       }
-      store_row(p, blk, h, G, e / (D / 4), e % (D / 4) * 4, x, sum);
+      store_row(p, it.first, it.r0 + r0 + e / (D / 4), it.h, G, e % (D / 4) * 4, x, sum);
     }
   }
 }

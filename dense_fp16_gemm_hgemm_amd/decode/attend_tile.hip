@@ -44,15 +44,15 @@ __device__ inline int piece_channel(int piece) {
 }
 
 template <int CODE, int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attend_tile_kernel(AttendArgs p, int blocks, int splits) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs p, int blocks, int splits) {
   constexpr int ROWS = 32 * NW, KS = D / 16, DT = D / 32, T = 64 * NW;
   constexpr int UNITS = kStage * D / 16, UN = (UNITS + T - 1) / T;  // 16-byte units of a stage, and a thread's
+  constexpr uint32_t kPart = part_bytes(ROWS, D);
   constexpr int VD = D / 4;                                         // groups of 4 channels
   __shared__ u32x4 kbuf[2][kStage * D / 8];
   __shared__ u32x4 vbuf[2][D * kStage / 8];
   __shared__ Meta meta[2];
   __shared__ unsigned long long nans[3];  // tokens of a stage with a NaN among their values' codes
-  __shared__ int last_flag;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -65,8 +65,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attend_tile_kernel(AttendArgs
   const int heads = p.batch.batch * H, bh = blockIdx.x % heads, rest = blockIdx.x / heads;
   const int j = rest % splits, rb = blocks - 1 - rest / splits, h = bh % H;
   const Block<kStage> blk = block_of<kStage>(p, G, ROWS, blocks, bh / H * blocks + rb, p.batch.batch * blocks);
-  if (blk.tiles == 0) return;
-  const int parts = min(splits, max(1, blk.tiles / 4));
+  const int parts = blk.tiles == 0 ? 0 : min(splits, max(1, blk.tiles / 4)), item = rb * heads + bh;
+  if (splits > 1 && j == 0 && tid == 0) {
+    const uint32_t at = (uint32_t)(item * splits) * kPart;
+    p.join[item] = parts > 1 ? JoinItem{blk.first, blk.r0, blk.rows, h, parts, at, at + kPart, kPart} : JoinItem{};
+  }
   if (j >= parts) return;
   const int s0 = (int)((int64_t)blk.tiles * j / parts), s1 = (int)((int64_t)blk.tiles * (j + 1) / parts);
   const int32_t* table = p.batch.table + (int64_t)blk.b * p.batch.table_stride;
@@ -407,14 +410,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attend_tile_kernel(AttendArgs
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           const f32x4 x = {o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]};
-          store_row(p, blk, h, G, row, 32 * d + 8 * a + 4 * hi, x * unit, l);
+          store_row(p, blk.first, blk.r0 + row, h, G, 32 * d + 8 * a + 4 * hi, x * unit, l);
         }
     return;
   }
-  constexpr uint32_t kPart = part_bytes<ROWS, D>();
   const auto parts_at = __builtin_amdgcn_make_buffer_rsrc(p.ws, (short)0, (int)MI_DECODE_WORKSPACE_BYTES, kRsrcWord3);
-  const int item = rb * heads + bh;
-  auto part = [&](int n) { return (uint32_t)(item * splits + n) * kPart; };
+  const uint32_t part = (uint32_t)(item * splits + j) * kPart;
   if (in) {
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -422,15 +423,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attend_tile_kernel(AttendArgs
       for (int a = 0; a < 4; ++a) {
         const f32x4 x = {o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]};
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x * unit), parts_at,
-                                               part(j) + 4 * (row * D + 32 * d + 8 * a + 4 * hi), 0, kDeviceScope);
+                                               part + 4 * (row * D + 32 * d + 8 * a + 4 * hi), 0, kDeviceScope);
       }
     if (hi == 0)
       __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{m, l}), parts_at,
-                                            part(j) + 4 * (ROWS * D + 2 * row), 0, kDeviceScope);
-  }
-  if (last_to_arrive(p.cnt + item, parts, &last_flag)) {
-    join_parts<kStage, ROWS, D, T>(p, parts_at, blk, h, G, parts, part, reinterpret_cast<float*>(&kbuf[0][0]));
-    if (tid == 0) __hip_atomic_store(p.cnt + item, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                                            part + 4 * (ROWS * D + 2 * row), 0, kDeviceScope);
   }
 }
 
@@ -442,19 +439,22 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   const int64_t items = blocks * a.batch.batch * a.cache.kv_heads;
   if (items > INT32_MAX) return hipErrorInvalidConfiguration;
   // Few items: their stages are split so that every compute unit has a piece.
-  int64_t splits = items < a.cus && items <= kCounters ? a.cus / items : 1;
+  int64_t splits = items < a.cus && items <= kJoins ? a.cus / items : 1;
   const int64_t stages = a.max_len / kStage + 1;
   if (splits > stages / 4) splits = stages / 4 > 0 ? stages / 4 : 1;
-  if (items * splits * part_bytes<ROWS, D>() > MI_DECODE_WORKSPACE_BYTES) splits = 1;
+  if (items * splits * part_bytes(ROWS, D) > MI_DECODE_WORKSPACE_BYTES) splits = 1;
   attend_tile_kernel<CODE, D, NW><<<(unsigned)(items * splits), 64 * NW, 0, s>>>(a, (int)blocks, (int)splits);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || splits == 1 ? e : launch_join(a, (int)items, ROWS, s);
 }
 
+// 256 channels: a row's sums, queries and logits need more registers than two
+// waves of a SIMD have.
 template <int CODE>
 hipError_t dims_of(const AttendArgs& a, hipStream_t s) {
   if (a.cache.head_dim == 64) return run<CODE, 64, 8>(a, s);
   if (a.cache.head_dim == 128) return run<CODE, 128, 8>(a, s);
-  return run<CODE, 256, 8>(a, s);
+  return run<CODE, 256, 4>(a, s);
 }
 
 }  // namespace

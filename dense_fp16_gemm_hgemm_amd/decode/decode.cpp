@@ -44,7 +44,7 @@ struct mi_decode_ctx {
   int cus = 0;
   bool no_device = false;
   float* ws = nullptr;
-  int* cnt = nullptr;
+  int* cnt = nullptr;  // counters, then the list of joins
   int last_hip_error = 0;
   std::mutex mu;  // guards last_hip_error
 };
@@ -122,7 +122,7 @@ mi_decode_status_t mi_decode_create(mi_decode_handle_t* out, uint32_t flags) {
   void* ws = nullptr;
   void* cnt = nullptr;
   if (hipMalloc(&ws, MI_DECODE_WORKSPACE_BYTES) != hipSuccess ||
-      hipMalloc(&cnt, kCounters * sizeof(int)) != hipSuccess ||
+      hipMalloc(&cnt, kCounters * sizeof(int) + kJoins * sizeof(JoinItem)) != hipSuccess ||
       hipMemset(cnt, 0, kCounters * sizeof(int)) != hipSuccess || hipDeviceSynchronize() != hipSuccess) {
     if (ws) (void)hipFree(ws);
     if (cnt) (void)hipFree(cnt);
@@ -316,6 +316,7 @@ mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cac
   a.scale = scale;
   a.ws = h->ws;
   a.cnt = h->cnt;
+  a.join = reinterpret_cast<JoinItem*>(h->cnt + kCounters);
   a.cus = h->cus;
   DeviceGuard g(h->device);
   return done(h, launch_attend(a, (hipStream_t)stream));

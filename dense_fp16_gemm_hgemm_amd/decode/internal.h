@@ -39,6 +39,13 @@ struct ReadArgs : KvArgs {
   void* v_out;
 };
 
+// A row block whose result lies in parts (parts 0: none): rows r0 .. r0 + rows - 1
+// of the sequence whose first token is `first`, of key-value head h.
+struct JoinItem {
+  int32_t first, r0, rows, h, parts;
+  uint32_t head, tail, step;  // bytes in the workspace: part 0, part 1, and from part to part
+};
+
 struct AttendArgs : KvArgs {
   mi_decode_rows_t q, out;
   int64_t max_len;
@@ -46,6 +53,7 @@ struct AttendArgs : KvArgs {
   float scale;
   float* ws;  // partial results, MI_DECODE_WORKSPACE_BYTES
   int* cnt;   // arrival counters, zero between launches
+  JoinItem* join;  // what a second kernel joins, or nullptr: the last workgroup does
   int cus;    // the device's compute units
 };
 
@@ -56,6 +64,9 @@ hipError_t launch_read(const ReadArgs& a, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s);       // any number of rows
 hipError_t launch_attend_tile(const AttendArgs& a, hipStream_t s);  // many rows a sequence
 
-constexpr int kCounters = 65536;
+// Adds the parts of `items` listed blocks of at most block_rows rows.
+hipError_t launch_join(const AttendArgs& a, int items, int block_rows, hipStream_t s);
+
+constexpr int kCounters = 1024, kJoins = 1024;  // workgroups or row blocks with parts
 
 }  // namespace mid
