@@ -43,6 +43,18 @@ __device__ inline int piece_channel(int piece) {
   return piece < D / 16 ? 16 * piece : 16 * (piece - D / 16) + 8;
 }
 
+// The order of N products and the reads of their left operands, AHEAD reads in front.
+template <int N, int AHEAD>
+__device__ inline void schedule_reads() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
+}
+
 template <int CODE, int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs p, int blocks, int splits) {
   constexpr int ROWS = 32 * NW, KS = D / 16, DT = D / 32, T = 64 * NW;
@@ -283,7 +295,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     for (int d = 0; d < DT; ++d) o[d] *= down;
   };
   auto use = [&](int n, int b, int n3) {
-    const Meta& mt = meta[b];
+    const Meta mt = meta[b];
     const float down = mt.down;
     if (down != 1.f) rescale(down);
     const int t0 = blk.token(n);
@@ -304,8 +316,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
       for (int x = 0; x < 2; ++x) {
         const u32x4 k = kb[kx[s % 4] + (x * 32 * (D / 8) + s / 4 * 8)];
         z[x] = mma(__builtin_bit_cast(h8, k), qf[s], z[x]);
-        if (s % 4 == 3 && x) __builtin_amdgcn_sched_barrier(0);
       }
+    // operands are read six products ahead of their use
+    schedule_reads<2 * KS, 6>();
     float f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = fac * mt.ks[i];
@@ -339,6 +352,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     }
     h8 pf[4];
     if (whole) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float c = mt.lv[i] - m;
@@ -354,13 +368,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     } else {
       const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const float v = mt.vr[i];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float y = z[i / 2][8 * (i % 2) + e], w = __builtin_amdgcn_exp2f(y - base);
           l += w;
-          pf[i][e] = y == -INFINITY ? (_Float16)0 : (_Float16)(w * mt.vr[i]);
+          pf[i][e] = y == -INFINITY ? (_Float16)0 : (_Float16)(w * v);
         }
+      }
     }
     if (CODE == MI_DECODE_E4M3 && nans[n3]) {
 #pragma unroll
@@ -371,14 +387,15 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
           if ((nans[n3] >> (4 * hi) >> at & 1) && (valid >> i & 1) && seen(at)) pf[i][e] = (_Float16)NAN;
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const u32x4 v = vb[vx[i ^ (2 * (d & 1))] + d * 32 * (kStage / 8)];
         o[d] = mma(__builtin_bit_cast(h8, v), pf[i], o[d]);
-        if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
+    schedule_reads<4 * DT, 6>();
   };
 
   const bool first_half = wave < NW / 2;
