@@ -23,16 +23,10 @@ namespace {
 
 constexpr int kStage = 64;
 
-// The four 16-token parts of a stage.
-struct Meta {
-  float ks[4];   // key scales, 0 where there is no page
-  float vr[4];   // value scales in units of vmax
-  float lv[4];   // their logarithms
-  float iv[4];   // 1 / vr
-  int valid;     // bit i: part i has a page
-  int odd;       // a scale is zero, negative or not finite
-  float down;    // what sums in the unit of the stage before are multiplied by
-  float vmax;    // the unit
+// What a stage's buffer says of one of its four 16-token parts.
+struct Part {
+  float ks, vs;  // scales of its page, 0 where there is none
+  int page;      // the page, or -1
 };
 
 // Channels of a token lie in 16-byte pieces, the first halves of all 16-channel
@@ -63,7 +57,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   constexpr int VD = D / 4;                                         // groups of 4 channels
   __shared__ u32x4 kbuf[2][kStage * D / 8];
   __shared__ u32x4 vbuf[2][D * kStage / 8];
-  __shared__ Meta meta[2];
+  __shared__ Part part_of[2][4];
   __shared__ unsigned long long nans[3];  // tokens of a stage with a NaN among their values' codes
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -86,69 +80,58 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   const int s0 = (int)((int64_t)blk.tiles * j / parts), s1 = (int)((int64_t)blk.tiles * (j + 1) / parts);
   const int32_t* table = p.batch.table + (int64_t)blk.b * p.batch.table_stride;
 
-  auto valid_page = [&](int entry) { return entry >= 0 && (int64_t)entry < p.cache.pages ? entry : -1; };
-  // the table's entry for token tok of stage n, -1 where no row sees its part
+  // What a wave loads and converts belongs to one 16-token part for each i, so
+  // pages and addresses are the same in all its lanes: units of 16 codes of a
+  // token's key, and of 4 tokens by 4 channels of values.
+  const bool loader = UNITS >= T || wave < UNITS / 64;
   const int log_ps = __builtin_ctz((unsigned)ps);
-  auto entry = [&](int n, int tok) {
-    const int at = blk.token(n) + (tok & ~15);
-    const bool some = n < s1 && at <= blk.phi && (p.window == 0 || at + 15 > blk.plo - p.window || at < p.sinks);
-    int e = -1;
-    if (some) e = table[at >> log_ps];
-    return e;
-  };
-  // a page's bytes fit 32 bits: 65535 heads of 256 tokens of 256 channels
-  const uint32_t head_bytes = (uint32_t)(ps * D), page_bytes = (uint32_t)H * head_bytes;
-  auto place = [&](const void* base, int n, int tok, int e) {
-    const int page = valid_page(e);
-    const uint8_t* head = static_cast<const uint8_t*>(base) + (uint64_t)h * head_bytes;
-    const uint8_t* at = head + (uint64_t)(uint32_t)page * page_bytes + (((blk.token(n) + tok) & (ps - 1)) * D);
-    return page >= 0 ? at : reinterpret_cast<const uint8_t*>(p.ws);
-  };
-
-  // what a thread loads and converts: units of 16 codes of a token's key, and of
-  // 4 tokens by 4 channels of values
-  int ke[UN], ve[UN], me = -1;  // table entries, one stage ahead of the loads
+  const uint32_t head_bytes = (uint32_t)(ps * D);  // a page's bytes fit 32 bits: 65535 heads of 256 x 256
+  const uint32_t page_bytes = (uint32_t)H * head_bytes;
+  const uint32_t koff = (tid / (D / 16) & 15) * D + tid % (D / 16) * 16;
+  const uint32_t voff = (tid / VD & 3) * 4 * D + tid % VD * 4;
+  auto part = [&](int i) { return (64 * wave + T * i) / D; };
+  int entry[UN];  // table entries, one stage ahead of the loads; -1: no row sees the part
   u32x4 kraw[UN];
   uint32_t vraw[UN][4];
-  float mk = 0.f, mv = 0.f, vmax = 0.f;  // scales of part `tid` of a stage, in threads 0..3
-  int mpage = -1;
+  Part got[UN];
   auto entries = [&](int n) {
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      const int u = tid + T * i;
-      if (UNITS < T && u >= UNITS) break;
-      ke[i] = entry(n, u / (D / 16));
-      ve[i] = entry(n, u / VD * 4);
+      const int at = blk.token(n) + 16 * part(i);
+      entry[i] = -1;
+      if (loader && n < s1 && at <= blk.phi && (p.window == 0 || at + 15 > blk.plo - p.window || at < p.sinks))
+        entry[i] = table[at >> log_ps];
     }
-    if (tid < 4) me = entry(n, 16 * tid);
   };
   auto loads = [&](int n) {
+    if (!loader) return;
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      const int u = tid + T * i;
-      if (UNITS < T && u >= UNITS) break;
-      kraw[i] = *reinterpret_cast<const u32x4*>(place(p.cache.k, n, u / (D / 16), ke[i]) + u % (D / 16) * 16);
-      const uint8_t* v = place(p.cache.v, n, u / VD * 4, ve[i]) + u % VD * 4;
+      int page = __builtin_amdgcn_readfirstlane(entry[i]);
+      if ((int64_t)page >= p.cache.pages) page = -1;
+      const int slot = (blk.token(n) + 16 * part(i)) & (ps - 1);
+      const uint64_t at = (uint64_t)(uint32_t)page * page_bytes + (uint32_t)h * head_bytes + (uint32_t)(slot * D);
+      // where there is no page, readable memory that is masked later
+      const uint8_t* k = page >= 0 ? static_cast<const uint8_t*>(p.cache.k) + at : reinterpret_cast<const uint8_t*>(p.ws);
+      const uint8_t* v = page >= 0 ? static_cast<const uint8_t*>(p.cache.v) + at : reinterpret_cast<const uint8_t*>(p.ws);
+      kraw[i] = *reinterpret_cast<const u32x4*>(k + koff);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) vraw[i][e] = *reinterpret_cast<const uint32_t*>(v + e * D);
-    }
-    if (tid < 4) {
-      mpage = valid_page(me);
-      mk = mv = 0.f;
-      if (mpage >= 0) {
-        const int64_t at = (int64_t)mpage * H + h;
-        mk = p.cache.k_scale[at];
-        mv = p.cache.v_scale[at];
+      for (int e = 0; e < 4; ++e) vraw[i][e] = *reinterpret_cast<const uint32_t*>(v + voff + e * D);
+      got[i] = Part{0.f, 0.f, page};
+      if (page >= 0 && (64 * wave + T * i) % D == 0) {  // the part's first wave
+        got[i].ks = p.cache.k_scale[(int64_t)page * H + h];
+        got[i].vs = p.cache.v_scale[(int64_t)page * H + h];
       }
     }
   };
   // codes of a stage to operands in buffer b
   auto convert = [&](int b, int n3) {
+    if (!loader) return;
     bool any_nan = false;
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
+      if (lane == 0 && (64 * wave + T * i) % D == 0) part_of[b][part(i)] = got[i];
       const int u = tid + T * i;
-      if (UNITS < T && u >= UNITS) break;
       const int tok = u / (D / 16), c = u % (D / 16);
       u32x4* row = &kbuf[b][tok * (D / 8)];
       row[c ^ (tok & 7)] = __builtin_bit_cast(u32x4, along<CODE>(kraw[i][0], kraw[i][1]));
@@ -200,23 +183,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
         u32x2* to = reinterpret_cast<u32x2*>(&vbuf[b][dim * (kStage / 8) + (piece ^ ((dim ^ (dim >> 3)) & 7))]) + half;
         *to = u32x2{lo[y], hi4[y]};
       }
-    }
-    if (wave == 0) {
-      const bool mine = tid < 4;
-      float top = mine && fabsf(mv) < INFINITY ? fabsf(mv) : 0.f;
-      top = fmaxf(top, __shfl_xor(top, 1));
-      top = fmaxf(top, __shfl_xor(top, 2));
-      const float down = top > vmax ? vmax / top : 1.f;
-      vmax = fmaxf(vmax, top);
-      const float vr = mv / (vmax > 0.f ? vmax : 1.f);
-      const bool page = mine && mpage >= 0;
-      const bool odd = page && !(vr > 0.f && vr < INFINITY && mk >= 0.f && mk < INFINITY);
-      const int odds = __ballot(odd) & 15, valids = __ballot(page) & 15;
-      if (mine) {
-        meta[b].ks[tid] = mk, meta[b].vr[tid] = vr;
-        meta[b].lv[tid] = __builtin_amdgcn_logf(vr), meta[b].iv[tid] = 1.f / vr;
-      }
-      if (tid == 0) meta[b].valid = valids, meta[b].odd = odds, meta[b].down = down, meta[b].vmax = vmax;
     }
   };
 
@@ -273,7 +239,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   entries(s0 + 2);
   __syncthreads();
 
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, vmax = 0.f, log_vmax = 0.f;
   f32x16 o[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = f32x16{};
@@ -295,19 +261,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     for (int d = 0; d < DT; ++d) o[d] *= down;
   };
   auto use = [&](int n, int b, int n3) {
-    const Meta mt = meta[b];
-    const float down = mt.down;
-    if (down != 1.f) rescale(down);
     const int t0 = blk.token(n);
     if (wrows <= 0 || t0 > whi) return;
     if (p.window && t0 + kStage - 1 <= wlo - p.window && t0 >= p.sinks) return;
-    // Token c after the lane's first one (constants, compared with numbers of
-    // the stage: left as tokens, 32 of them would stay in registers).
-    const int upto = pos - t0 - 4 * hi, after = p.window ? upto - p.window : -1, sink = p.sinks - t0 - 4 * hi;
-    auto seen = [&](int c) { return c <= upto && (c > after || c < sink); };
-    const int valid = mt.valid;
-    const bool whole = valid == 15 && mt.odd == 0 && t0 + kStage - 1 <= wlo &&
-                       (p.window == 0 || t0 > whi - p.window || t0 + kStage - 1 < p.sinks);
+    // Lane i knows part i % 4; read before the first product's operands, used after it.
+    const Part mine = part_of[b][lane & 3];
+    __builtin_amdgcn_sched_barrier(0);
     const u32x4 *kb = kbuf[b], *vb = vbuf[b];
     f32x16 z[2] = {};
 #pragma unroll
@@ -319,9 +278,28 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
       }
     // operands are read six products ahead of their use
     schedule_reads<2 * KS, 6>();
+    // Sums are in units of the largest finite value scale so far.
+    const bool finite = fabsf(mine.vs) < INFINITY;
+    if (__any(finite && fabsf(mine.vs) > vmax)) {
+      float top = finite ? fabsf(mine.vs) : 0.f;
+      top = fmaxf(top, __shfl_xor(top, 1));
+      top = fmaxf(top, __shfl_xor(top, 2));
+      rescale(vmax / top);
+      vmax = top;
+      log_vmax = __builtin_amdgcn_logf(top);
+    }
+    // Token c after the lane's first one (constants, compared with numbers of
+    // the stage: left as tokens, 32 of them would stay in registers).
+    const int upto = pos - t0 - 4 * hi, after = p.window ? upto - p.window : -1, sink = p.sinks - t0 - 4 * hi;
+    auto seen = [&](int c) { return c <= upto && (c > after || c < sink); };
+    const int valid = __ballot(mine.page >= 0) & 15;
+    // scales that have a logarithm, and a reciprocal in the unit
+    const bool plain = mine.vs >= 0x1p-126f && mine.vs >= vmax * 0x1p-64f && mine.vs < INFINITY && mine.ks >= 0.f && mine.ks < INFINITY;
+    const bool whole = valid == 15 && __all(plain) && t0 + kStage - 1 <= wlo &&
+                       (p.window == 0 || t0 > whi - p.window || t0 + kStage - 1 < p.sinks);
     float f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = fac * mt.ks[i];
+    for (int i = 0; i < 4; ++i) f[i] = fac * lane_value(mine.ks, i);
     float top = -INFINITY;
     if (whole) {
 #pragma unroll
@@ -353,9 +331,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     h8 pf[4];
     if (whole) {
       __builtin_amdgcn_sched_barrier(0);
+      const float lv = __builtin_amdgcn_logf(mine.vs) - log_vmax, iv = vmax * __builtin_amdgcn_rcpf(mine.vs);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float c = mt.lv[i] - m;
+        const float c = lane_value(lv, i) - m;
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -363,13 +342,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
           sum += w;
           pf[i][e] = (_Float16)w;
         }
-        l = __builtin_fmaf(sum, mt.iv[i], l);
+        l = __builtin_fmaf(sum, lane_value(iv, i), l);
       }
     } else {
-      const float base = m == -INFINITY ? 0.f : m;
+      const float base = m == -INFINITY ? 0.f : m, vr = mine.vs / (vmax > 0.f ? vmax : 1.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float v = mt.vr[i];
+        const float v = lane_value(vr, i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float y = z[i / 2][8 * (i % 2) + e], w = __builtin_amdgcn_exp2f(y - base);
@@ -418,7 +397,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
 
   // o as rows: lane (col, hi) holds channels 32 d + 8 a + 4 hi + 0..3 of row col
   l += __shfl_xor(l, 32);
-  float unit = meta[(s1 - 1 - s0) & 1].vmax;
+  float unit = vmax;
   if (CODE == MI_DECODE_INT8) unit *= 1.f / kTiny;
   if (parts == 1) {
     if (in)
@@ -432,7 +411,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     return;
   }
   const auto parts_at = __builtin_amdgcn_make_buffer_rsrc(p.ws, (short)0, (int)MI_DECODE_WORKSPACE_BYTES, kRsrcWord3);
-  const uint32_t part = (uint32_t)(item * splits + j) * kPart;
+  const uint32_t to = (uint32_t)(item * splits + j) * kPart;
   if (in) {
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -440,11 +419,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
       for (int a = 0; a < 4; ++a) {
         const f32x4 x = {o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]};
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x * unit), parts_at,
-                                               part + 4 * (row * D + 32 * d + 8 * a + 4 * hi), 0, kDeviceScope);
+                                               to + 4 * (row * D + 32 * d + 8 * a + 4 * hi), 0, kDeviceScope);
       }
     if (hi == 0)
       __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, f32x2{m, l}), parts_at,
-                                            part + 4 * (ROWS * D + 2 * row), 0, kDeviceScope);
+                                            to + 4 * (ROWS * D + 2 * row), 0, kDeviceScope);
   }
 }
 
