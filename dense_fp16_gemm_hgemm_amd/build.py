@@ -9,8 +9,9 @@ It also builds ``dense_fp16_gemm_hgemm_amd/libmi_overlap.so`` (the load/compute
 overlap micro-benchmark, ``overlap/overlap.hip``),
 ``dense_fp16_gemm_hgemm_amd/libmi_ceiling.so`` (the MFMA, copy and HBM read
 ceilings, ``ceiling/ceiling.hip``), ``dense_fp16_gemm_hgemm_amd/libmi_decode.so``
-(the decode operators, ``decode/``) and, where rocBLAS is
-installed, ``dense_fp16_gemm_hgemm_amd/mi_hgemm_serve``, the server-mode load
+(the decode operators, ``decode/``), their calls from torch tensors,
+``dense_fp16_gemm_hgemm_amd/_decode_calls.so`` (``bind/decode_calls.cpp``, a
+Python extension module compiled with g++) and, where rocBLAS is installed, ``dense_fp16_gemm_hgemm_amd/mi_hgemm_serve``, the server-mode load
 generator (``serve/serve_bench.cpp``), linked against the library (found beside
 it at run time) and rocBLAS (the vendor backend it compares with).  Without
 rocBLAS the load generator is skipped with a note and the build still succeeds
@@ -37,6 +38,8 @@ CEILING_SRC = os.path.join(PKG, "ceiling", "ceiling.hip")
 CEILING_PATH = os.path.join(PKG, "libmi_ceiling.so")
 DECODE_SRC = os.path.join(PKG, "decode")
 DECODE_PATH = os.path.join(PKG, "libmi_decode.so")
+CALLS_SRC = os.path.join(PKG, "bind", "decode_calls.cpp")
+CALLS_PATH = os.path.join(PKG, "_decode_calls.so")
 SERVE_SRC = os.path.join(PKG, "serve", "serve_bench.cpp")
 SERVE_PATH = os.path.join(PKG, "mi_hgemm_serve")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -72,6 +75,24 @@ def _compile_cmds(folder=CSRC, prefix=""):
     return cmds
 
 
+def _build_calls() -> None:
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", os.path.join(ROOT, "include"),
+           *["-I" + d for d in cpp_extension.include_paths()], "-I/opt/rocm/include",
+           "-I" + sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp, "-L" + PKG, "-lmi_decode", "-L" + lib,
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        print(r.stdout.decode(errors="replace"), file=sys.stderr)
+        raise RuntimeError("g++ failed for " + CALLS_SRC)
+    os.replace(tmp, CALLS_PATH)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source and link the shared library; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -105,6 +126,7 @@ def build(verbose: bool = False) -> str:
     subprocess.run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp,
                     *[obj for _, obj, _ in decode_cmds]], check=True)
     os.replace(tmp, DECODE_PATH)
+    _build_calls()
     tmp = OVERLAP_PATH + ".tmp%d" % os.getpid()
     # Every inner loop starts on a 64-byte boundary.  The modes' FMA loops are
     # the same nine instructions; left where the compiler put them, two of the

@@ -7,8 +7,10 @@
 * ``Decode.kv_attend``  -- attention over that cache (grouped heads, causal, a window with
   first tokens that stay visible), one query a sequence or ragged many.
 
-Operations, layouts and rules are those of ``include/mi_decode.h``; this module checks
-arguments and marshals them: torch supplies device memory and the stream.  A call returns
+Operations, layouts and rules are those of ``include/mi_decode.h``; torch supplies device
+memory and the stream.  The four calls check and marshal their arguments in an extension
+module (``bind/decode_calls.cpp``), because a decode step's kernels take microseconds; the
+rest of the library is reached with ctypes.  A call returns
 without synchronising, and every call may be captured into a graph.  ``kv_attend`` uses the
 handle's workspace: calls that may overlap on different streams need handles of their own.
 
@@ -37,6 +39,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmi_decod
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python dense_fp16_gemm_hgemm_amd/build.py`")
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _decode_calls as _calls  # noqa: E402  (needs torch and the library above)
 
 MI_DECODE_OK = 0
 MI_DECODE_ERR_INVALID_ARG = 1
@@ -113,30 +116,15 @@ def _on(device, **tensors):
             raise ValueError(f"{name} must be on {device}, got {x.device}")
 
 
-def _rows(x, name, heads, head_dim, dtype):
-    """[tokens, heads, head_dim] with a contiguous last dimension, as the C struct."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != head_dim:
-        raise ValueError(f"{name} must have shape [tokens, {heads}, {head_dim}], got {tuple(x.shape)}")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    st, sh, sd = x.stride()
-    if sd != 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    return _Rows(x.data_ptr(), st, sh)
+def _raw(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
-def _int32(x, name, dim):
-    if x.dtype != torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {x.dtype}")
-    if x.dim() != dim or (x.numel() and x.stride(-1) != 1):
-        raise ValueError(f"{name} must have {dim} dimension(s), the last one contiguous")
-    return x.data_ptr()
-
-
-def _stream_ptr(stream, device):
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+def _done(result, what):
+    """A call's result, or DecodeError for the status that the library returned."""
+    if type(result) is int:
+        raise DecodeError(result, what)
+    return result
 
 
 # ------------------------------------------------------- 4-bit weights --
@@ -233,7 +221,7 @@ class KvCache:
     page's and head's scale."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim",
-                 "device", "_struct", "_ref")
+                 "device", "_struct", "_at", "_dev")
 
     def __init__(self, k, v, k_scale, v_scale):
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
@@ -255,7 +243,7 @@ class KvCache:
         self.device = k.device
         self._struct = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                               self.pages, self.kv_heads, self.page_size, self.head_dim, _CODES[k.dtype])
-        self._ref = _byref(self._struct)
+        self._at, self._dev = ctypes.addressof(self._struct), k.device.index
 
     @classmethod
     def empty(cls, pages, kv_heads, head_dim, page_size=64, dtype=torch.int8, device="cuda"):
@@ -264,25 +252,6 @@ class KvCache:
                                     device=device).view(dtype)
         scale = lambda: torch.zeros((pages, kv_heads), dtype=torch.float32, device=device)  # noqa: E731
         return cls(codes(), codes(), scale(), scale())
-
-
-def _batch(cache, table, lens, cu, tokens, most, names):
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    lp, tp = _int32(lens, names[0], 1), _int32(table, "table", 2)
-    if table.shape[0] != B:
-        raise ValueError(f"table must have one row a sequence ({B}), got {table.shape[0]}")
-    if cu is None:
-        if tokens != B or most != 1:
-            raise ValueError(f"without {names[1]} each of the {B} sequences has one token, got {tokens}")
-        cp = None
-    else:
-        cp = _int32(cu, names[1], 1)
-        if cu.shape[0] != B + 1:
-            raise ValueError(f"{names[1]} must have {B + 1} entries, got {cu.shape[0]}")
-    dev = cache.device
-    if lens.device != dev or table.device != dev or (cu is not None and cu.device != dev):
-        raise ValueError(f"table, {names[0]} and {names[1]} must be on {dev}")
-    return _Batch(tp, lp, cp, table.stride(0) if B > 1 else table.shape[1], table.shape[1], B, tokens, most)
 
 
 # -------------------------------------------------------------- handle --
@@ -317,68 +286,15 @@ class Decode:
 
     def w4_linear(self, x, qweight, scales, zeros=None, *, n, group=128, bias=None, out=None, stream=None):
         """x [M, K] times the 4-bit weights [n, K]: [M, n] in x's type, sums in float32."""
-        if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-            raise ValueError("x must be 2-D with unit-stride rows")
-        dt, dev = _dtype(x, "x"), x.device
-        M, K = x.shape
-        if not x.is_cuda:
-            raise ValueError("x must be on the GPU")
-        if group < 32 or group % 32:
-            raise ValueError(f"group must be a positive multiple of 32, got {group}")
-        nb, shape = -(-n // 16), (-(-K // group), -(-n // 16) * 16)
-        if qweight.dtype != torch.int32 or tuple(qweight.shape) != (nb, -(-K // 128), 64, 4) or not qweight.is_contiguous():
-            raise ValueError(f"qweight must be contiguous int32 {(nb, -(-K // 128), 64, 4)} for n={n}, K={K}")
-        if scales.dtype != x.dtype or tuple(scales.shape) != shape or not scales.is_contiguous():
-            raise ValueError(f"scales must be contiguous {x.dtype} {shape}")
-        if zeros is not None and (zeros.dtype != torch.uint8 or tuple(zeros.shape) != shape or not zeros.is_contiguous()):
-            raise ValueError(f"zeros must be contiguous uint8 {shape}")
-        if bias is not None and (bias.dtype != x.dtype or tuple(bias.shape) != (n,) or (n > 1 and bias.stride(0) != 1)):
-            raise ValueError(f"bias must be contiguous {x.dtype} {(n,)}")
-        if out is None:
-            out = torch.empty((M, n), dtype=x.dtype, device=dev)
-        elif tuple(out.shape) != (M, n) or out.dtype != x.dtype or (n > 1 and out.stride(1) != 1):
-            raise ValueError(f"out must be {x.dtype} {(M, n)} with unit-stride rows")
-        _on(dev, qweight=qweight, scales=scales, zeros=zeros, bias=bias, out=out)
-        _check(_w4_linear(self.handle, dt, M, n, K, group, x.data_ptr(), x.stride(0), qweight.data_ptr(),
-                          scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-                          None if bias is None else bias.data_ptr(), out.data_ptr(), out.stride(0),
-                          _stream_ptr(stream, dev)), "mi_decode_w4_linear")
-        return out
+        return _done(_calls.w4_linear(self.handle, x, qweight, scales, zeros, n, group, bias, out, _raw(stream)),
+                     "mi_decode_w4_linear")
 
     def kv_append(self, cache, k, v, table, past, cu_new=None, max_new=1, *, q=None, rope=None,
                   interleaved=False, q_out=None, stream=None):
         """Append k and v [tokens, kv_heads, head_dim] after the `past` tokens of each sequence;
         returns q [tokens, q_heads, head_dim] turned by its positions (None without q)."""
-        dt, H, D, dev = _dtype(k, "k"), cache.kv_heads, cache.head_dim, cache.device
-        T = k.shape[0]
-        rk, rv = _rows(k, "k", H, D, k.dtype), _rows(v, "v", H, D, k.dtype)
-        if v.shape[0] != T:
-            raise ValueError("k and v must have the same tokens")
-        batch = _batch(cache, table, past, cu_new, T, max_new, ("past", "cu_new"))
-        rq = ro = rp = None
-        hq = rows = rot = 0
-        if q is not None:
-            hq = q.shape[1] if q.dim() == 3 else -1
-            rq = _rows(q, "q", hq, D, k.dtype)
-            if q.shape[0] != T:
-                raise ValueError("q must have k's tokens")
-            if q_out is None:
-                q_out = torch.empty((T, hq, D), dtype=q.dtype, device=dev)
-            elif tuple(q_out.shape) != (T, hq, D):
-                raise ValueError(f"q_out must have shape {(T, hq, D)}")
-            ro = _rows(q_out, "q_out", hq, D, k.dtype)
-            rq, ro = _byref(rq), _byref(ro)
-        if rope is not None:
-            if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
-                raise ValueError("rope must be a contiguous float32 [positions, rot_dim] table")
-            rows, rot = rope.shape
-            if rows < table.shape[1] * cache.page_size:
-                raise ValueError(f"rope has {rows} positions, the table has {table.shape[1] * cache.page_size}")
-            rp = rope.data_ptr()
-        _on(dev, k=k, v=v, q=q, q_out=q_out, rope=rope)
-        _check(_kv_append(self.handle, cache._ref, dt, _byref(batch), _byref(rk), _byref(rv), rp, rows, rot,
-                          bool(interleaved), hq, rq, ro, _stream_ptr(stream, dev)), "mi_decode_kv_append")
-        return q_out if q is not None else None
+        return _done(_calls.kv_append(self.handle, cache._at, cache._dev, k, v, table, past, cu_new, max_new, q, rope,
+                                      interleaved, q_out, _raw(stream)), "mi_decode_kv_append")
 
     def kv_read(self, cache, table, start, cu=None, *, tokens=None, max_tokens=None, dtype=torch.float16,
                 stream=None):
@@ -388,38 +304,12 @@ class Decode:
             raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
         T = start.shape[0] if tokens is None else tokens
         most = (1 if cu is None else T) if max_tokens is None else max_tokens
-        batch = _batch(cache, table, start, cu, T, most, ("start", "cu"))
-        shape = (T, cache.kv_heads, cache.head_dim)
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
-        _check(_kv_read(self.handle, cache._ref, _DTYPES[dtype], _byref(batch), k.data_ptr(), v.data_ptr(),
-                        _stream_ptr(stream, cache.device)), "mi_decode_kv_read")
-        return k, v
+        return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, T, most,
+                                    dtype == torch.bfloat16, _raw(stream)), "mi_decode_kv_read")
 
     def kv_attend(self, q, cache, table, lens, cu_q=None, max_q=1, *, max_len=None, window=0, sinks=0,
                   scale=None, out=None, stream=None):
         """softmax(scale q k^T) v over the cache for q [tokens, q_heads, head_dim]: each
         sequence's queries are the last of its lens[b] tokens.  scale: head_dim ** -0.5."""
-        D, dev = cache.head_dim, cache.device
-        dt = _dtype(q, "q")
-        hq = q.shape[1] if q.dim() == 3 else -1
-        rq = _rows(q, "q", hq, D, q.dtype)
-        T = q.shape[0]
-        if hq < 1 or hq % cache.kv_heads:
-            raise ValueError(f"q must have a multiple of {cache.kv_heads} heads, got {hq}")
-        if window < 0 or sinks < 0:
-            raise ValueError("window and sinks must not be negative")
-        batch = _batch(cache, table, lens, cu_q, T, max_q, ("lens", "cu_q"))
-        if out is None:
-            out = torch.empty((T, hq, D), dtype=q.dtype, device=dev)
-        elif out.shape[0] != T:
-            raise ValueError("out must have q's tokens")
-        ro = _rows(out, "out", hq, D, q.dtype)
-        if q.device != dev or out.device != dev:
-            raise ValueError(f"q and out must be on {dev}")
-        if max_len is None:
-            max_len = table.shape[1] * cache.page_size
-        _check(_kv_attend(self.handle, cache._ref, dt, _byref(batch), max_len, hq, _byref(rq), _byref(ro),
-                          D ** -0.5 if scale is None else scale, window, sinks, _stream_ptr(stream, dev)),
-               "mi_decode_kv_attend")
-        return out
+        return _done(_calls.kv_attend(self.handle, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
+                                      window, sinks, scale, out, _raw(stream)), "mi_decode_kv_attend")
