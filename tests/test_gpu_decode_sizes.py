@@ -1,0 +1,128 @@
+"""Decode operators where a call's tokens, rows or sequences are many, and NaN that only some rows see."""
+import pytest
+import torch
+
+from decode_ref import F, attend, half_step, layout, random_codes, take_pages, values
+
+pytestmark = pytest.mark.gpu
+decode = pytest.importorskip("dense_fp16_gemm_hgemm_amd.decode")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+from test_gpu_decode_attend import check, make, put  # noqa: E402
+
+DEV = torch.device("cuda", 0)
+CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
+@pytest.fixture(scope="module")
+def d():
+    h = decode.Decode()
+    yield h
+    h.close()
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("D, Hq, H, page, new", [(256, 4, 2, 64, [300, 1, 257, 0]), (256, 16, 1, 16, [40]),
+                                                 (128, 16, 1, 32, [33, 5]), (64, 5, 1, 128, [16, 200]),
+                                                 (128, 8, 8, 16, [65, 300])])
+def test_many_rows(d, D, Hq, H, page, new, codes):
+    print(f"many rows D={D} Hq={Hq} H={H} page={page} new={new} {codes}", flush=True)
+    past = [700, 0, 65, 9][:len(new)]
+    lens = [p + n for p, n in zip(past, new)]
+    cache, table, cu, q = make(lens, new, Hq, H, D, page, CODES[codes], torch.bfloat16, D + sum(new))
+    for window, sinks in ((0, 0), (50, 3)):
+        out = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), max(new), max_len=max(lens), window=window, sinks=sinks)
+        check(out, cache, q, table, lens, cu, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("D, Hq, H, new", [(128, 8, 1, 6), (128, 4, 2, 100), (64, 16, 2, 3), (256, 2, 1, 20), (256, 8, 1, 70)])
+def test_long_sequences_of_several_rows(d, D, Hq, H, new, codes):
+    """Few items, whose parts many workgroups compute and others add."""
+    print(f"long D={D} Hq={Hq} H={H} new={new} {codes}", flush=True)
+    lens = [21000, 64]
+    cache, table, cu, q = make(lens, [new, min(new, 64)], Hq, H, D, 64, CODES[codes], torch.float16, D + new)
+    dl, dt, dc = put(lens), table.to(DEV), put(cu)
+    out = d.kv_attend(q, cache, dt, dl, dc, new, max_len=max(lens))
+    check(out, cache, q, table, lens, cu)
+    for _ in range(3):
+        assert torch.equal(out, d.kv_attend(q, cache, dt, dl, dc, new, max_len=max(lens)))
+    one = d.kv_attend(q[-1:], cache, dt[1:], dl[1:])  # another split of the same workspace in between
+    check(one, cache, q[-1:], table[1:], lens[1:], [0, 1])
+    assert torch.equal(out, d.kv_attend(q, cache, dt, dl, dc, new, max_len=max(lens)))
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_many_sequences(d, new):
+    """More sequences than a wave has lanes, some of them empty."""
+    lens = [(37 * i) % 400 + new if i % 11 else 0 for i in range(150)]
+    tokens = [min(new, n) for n in lens]
+    cache, table, cu, q = make(lens, tokens, 8, 2, 64, 16, torch.int8, torch.float16, 2)
+    out = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new, max_len=max(lens))
+    check(out, cache, q, table, lens, cu)
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("D, Hq, H, new", [(64, 8, 1, 2), (128, 8, 1, 6), (128, 8, 1, 20), (64, 4, 1, 90), (256, 2, 1, 300)])
+@pytest.mark.parametrize("where", ["v", "k", "v_scale", "k_scale"])
+def test_nan_that_only_later_rows_see(d, where, D, Hq, H, new, codes):
+    """A token's NaN reaches the rows that see it and leaves the earlier ones as they were."""
+    if codes == "int8" and where in ("v", "k"):
+        return  # int8 has no NaN
+    print(f"nan {where} D={D} new={new} {codes}", flush=True)
+    lens, page = [400 + new], 16
+    cache, table, cu, q = make(lens, [new], Hq, H, D, page, CODES[codes], torch.float16, 31)
+    dt = table.to(DEV)
+    want = d.kv_attend(q, cache, dt, put(lens), put(cu), new)
+    at = lens[0] - 1 if where in ("v", "k") else (lens[0] - 1) // page * page  # a scale is its whole page's
+    pg = int(table[0, at // page])
+    if where in ("v", "k"):
+        getattr(cache, where).view(torch.uint8)[pg, :, at % page, 3] = 0x7f
+    else:
+        getattr(cache, where)[pg] = float("nan")
+    got = d.kv_attend(q, cache, dt, put(lens), put(cu), new)
+    first = max(at - (lens[0] - new), 0)  # the first query that sees it
+    assert torch.equal(got[:first], want[:first])
+    seen = torch.isnan(got[first:]) if where != "v" else torch.isnan(got[first:]).any(-1, keepdim=True)
+    assert torch.all(seen)
+
+
+@pytest.mark.parametrize("new", [1, 4])
+def test_append_and_read_many_sequences(d, new):
+    """150 sequences of 0 to `new` tokens: every position and page as if they came alone."""
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    B, H, D, page = 150, 2, 64, 16
+    past = [(29 * i) % 90 for i in range(B)]
+    tokens = [0 if i % 7 == 3 else 1 + i % new for i in range(B)]
+    lens = [p + n for p, n in zip(past, tokens)]
+    pages = sum(-(-n // page) for n in lens) + B
+    table = layout([n + 1 for n in lens], page, pages, torch.Generator().manual_seed(9))
+    cache = decode.KvCache.empty(pages, H, D, page)
+    cu = [0]
+    for n in tokens:
+        cu.append(cu[-1] + n)
+    T = cu[-1]
+    k, v, q = (torch.randn((T, h, D), device=DEV, generator=gen).half() for h in (H, H, 6))
+    rope = decode.rope_table(table.shape[1] * page, D)
+    turned = d.kv_append(cache, k, v, table.to(DEV), put(past), put(cu), new, q=q, rope=rope)
+    rk, rv = d.kv_read(cache, table.to(DEV), put(past), put(cu), tokens=T, max_tokens=new)
+    seq = [b for b, n in enumerate(tokens) for _ in range(n)]
+    pos = [past[b] + i for b, n in enumerate(tokens) for i in range(n)]
+    angle = torch.tensor(pos, device=DEV, dtype=F)[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device=DEV, dtype=F) / D)
+    co, si = angle.cos()[:, None], angle.sin()[:, None]
+
+    def rotated(x):
+        a, b = x.to(F)[..., :D // 2], x.to(F)[..., D // 2:]
+        return torch.cat([a * co - b * si, b * co + a * si], -1)
+
+    # the table's angles carry a rounding to binary32, products and sums three more
+    slack = 4 * 2.0 ** -24 * 8
+    assert torch.all((turned.to(F) - rotated(q)).abs() <= half_step(torch.float16) * (rotated(q).abs() + slack) + slack)
+    page_of = table[torch.tensor(seq), torch.tensor(pos) // page].long().to(DEV)
+    for have, want, which in ((rk, rotated(k), "k"), (rv, v.to(F), "v")):
+        scale = getattr(cache, which + "_scale")[page_of].to(F)[..., None]
+        bound = scale * (0.5 + 2.0 ** -20) + slack
+        assert torch.all((have.to(F) - want).abs() <= bound + half_step(torch.float16) * (want.abs() + bound))
+        # the page's scale is that of its largest new value
+        slot = values(take_pages(getattr(cache, which), page_of)).abs().amax((2, 3))
+        assert torch.all(slot == 127)
