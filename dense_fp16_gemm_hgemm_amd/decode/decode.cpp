@@ -172,8 +172,9 @@ mi_decode_status_t mi_decode_w4_linear(mi_decode_handle_t h, mi_decode_dtype_t d
                                        void* stream) {
   if (!h || M < 0 || N < 0 || K < 0 || group < 1) return MI_DECODE_ERR_INVALID_ARG;
   if (!is16(dtype) || group % 32) return MI_DECODE_ERR_UNSUPPORTED;
-  if (M > INT32_MAX || N > INT32_MAX - 15 || K > INT32_MAX - 127) return MI_DECODE_ERR_UNSUPPORTED;
+  if (M > INT32_MAX || N > INT32_MAX - 15 || K > (1 << 30)) return MI_DECODE_ERR_UNSUPPORTED;
   if ((M > 1 && ldx < K) || (M > 1 && ldy < N)) return MI_DECODE_ERR_INVALID_ARG;
+  if (M > 1 && ldx > (int64_t(1) << 25)) return MI_DECODE_ERR_UNSUPPORTED;  // 32 rows' bytes are counted in 32 bits
   if (M == 0 || N == 0) return MI_DECODE_OK;
   if (!y || (K > 0 && (!x || !qweight || !scales))) return MI_DECODE_ERR_INVALID_ARG;
   if (!aligned(qweight, 16) || !aligned(x, 2) || !aligned(y, 2) || !aligned(scales, 2) || !aligned(bias, 2))
@@ -192,7 +193,7 @@ mi_decode_status_t mi_decode_w4_linear(mi_decode_handle_t h, mi_decode_dtype_t d
   a.zeros = static_cast<const uint8_t*>(zeros);
   a.bias = bias;
   a.y = y;
-  a.ldx = ldx;
+  a.ldx = M > 1 ? ldx : 0;
   a.ldy = ldy;
   a.M = (int32_t)M;
   a.N = (int32_t)N;

@@ -30,8 +30,7 @@ namespace {
 
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
-constexpr int kRsrcWord3 = 0x00020000;
-constexpr uint32_t kOOB = 0x80000000u;
+typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));  // 16 bytes at any element
 
 template <bool BF16>
 __device__ inline f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
@@ -59,15 +58,14 @@ __device__ inline u32x4 unpack(uint32_t w, uint32_t base) {
 // columns in flight.  MW waves share a block and take 16 MT tokens each; the
 // other way round, waves that differ in K add their sums.  PER: matrix
 // instructions (32 columns each) to a group's sum.  R: loads of 4 tokens that
-// hold a wave's tokens.  WIDE: x's rows are 16-byte aligned and of whole
-// 16-byte pieces.
+// hold a wave's tokens.
 //
 // x comes in rows of 256 bytes (16 lanes), and goes through a piece of shared
 // memory that belongs to the wave: loaded as the matrix instruction wants it,
 // neighbouring lanes are in different rows, and each such load takes as many
 // cache lookups as it has lanes (16 x 4096 x 11008:
 // 15.6 us, through shared memory 12.7).
-template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX, bool WIDE>
+template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX>
 __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   constexpr int FL = 4 / PER;  // group sums to a block
   extern __shared__ float red[];
@@ -83,14 +81,14 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     wp[t] = reinterpret_cast<const u32x4*>(p.qw) + (int64_t)min(nb0 + t, NB - 1) * KB * 64;
-  const uint16_t* xb = static_cast<const uint16_t*>(p.x) + m0 * p.ldx;
-  // lane l holds 16-byte piece l % 16 of tokens l / 16, l / 16 + 4, ...
+  // Lane l holds the 16-byte piece l % 16 of tokens l / 16, l / 16 + 4, ...;
+  // rows may begin at any element (the hardware takes such loads as they are).
+  // Tokens past M read the last one's row and are not stored; a piece that
+  // crosses K is read 8 columns before K and shifted, one past K is zero.
   const int xrow = lane >> 4, xcol = lane & 15;
-  uint32_t xo[R];  // byte offset of the lane's row and column, or out of range
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    xo[i] = m0 + 4 * i + xrow < p.M ? (uint32_t)((4 * i + xrow) * p.ldx * 2 + xcol * 16) : kOOB;
-  const auto xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(xb), (short)0, (int)0x7fffffff, kRsrcWord3);
+  const uint8_t* xb = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.x) + m0 * p.ldx);
+  const uint32_t last = (uint32_t)(max(p.M - 1 - m0, 0) * p.ldx * 2), x0 = (uint32_t)(xrow * p.ldx * 2), x4 = (uint32_t)(p.ldx * 8);
+  if (m0 >= p.M) xb = static_cast<const uint8_t*>(p.x);
   // the wave's [16 MT][16] pieces; piece q of row i lies at q ^ (i % 16), so
   // that eight rows' pieces of one column do not meet in a bank
   u32x4* xs = reinterpret_cast<u32x4*>(red) + wave * (MT * 256);
@@ -124,24 +122,20 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
         zq[u][f][t] = (zp + row)[r];
       }
     }
-    const bool inside = kb * 128 + 128 <= p.K;
-    const int k = kb * 128 + xcol * 8;
+    const uint32_t piece = (uint32_t)min(at * 128 + xcol * 8, p.K - 8) * 2;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if constexpr (WIDE) {
-        const uint32_t off = inside || k < p.K ? xo[i] : kOOB;
-        xq[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, off, kb * 256, 0));
-      } else {
-        const uint16_t* row = xb + (int64_t)(4 * i + xrow) * p.ldx;
-        const bool row_in = m0 + 4 * i + xrow < p.M;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo = row_in && k + 2 * e < p.K ? row[k + 2 * e] : 0;
-          const uint32_t hi = row_in && k + 2 * e + 1 < p.K ? row[k + 2 * e + 1] : 0;
-          xq[u][i][e] = lo | hi << 16;
-        }
-      }
-    }
+    for (int i = 0; i < R; ++i) xq[u][i] = *reinterpret_cast<const loose*>(xb + (min(x0 + i * x4, last) + piece));
+  };
+  // what the piece of block kb that lies past K brought, taken out
+  auto trim = [&](u32x4 w, int kb) {
+    const int by = min(max(kb * 128 + xcol * 8 + 8 - p.K, 0), 8);  // columns past K
+    uint64_t lo = w[0] | (uint64_t)w[1] << 32, hi = w[2] | (uint64_t)w[3] << 32;
+    if (by & 4) lo = hi, hi = 0;
+    const int bits = 16 * (by & 3);
+    lo = bits ? lo >> bits | hi << (64 - bits) : lo;
+    hi >>= bits;
+    if (by == 8) lo = hi = 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   };
 
   f32x4 total[MT][NT];
@@ -160,6 +154,14 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (base + u * KW >= KB) break;
+      const int kb = base + u * KW;
+      if (kb * 128 + 128 > p.K) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          xq[u][i] = trim(xq[u][i], kb);
+          __builtin_amdgcn_sched_barrier(0);  // one at a time: together they need 8 R more registers
+        }
+      }
 #pragma unroll
       for (int i = 0; i < R; ++i) xs[(4 * i + xrow) * 16 + (xcol ^ ((4 * i + xrow) & 15))] = xq[u][i];
       u32x4 xf[4][MT];
@@ -230,19 +232,31 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   }
 }
 
-// K = 0: the bias, or zeros.
+// K below 8, where no whole piece of a row exists: one result to a thread.
 template <bool BF16>
-__global__ __launch_bounds__(256) void w4_bias_kernel(W4Args p) {
+__global__ __launch_bounds__(256) void w4_short_kernel(W4Args p) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)p.M * p.N) return;
   const int n = (int)(i % p.N);
-  static_cast<uint16_t*>(p.y)[i / p.N * p.ldy + n] = p.bias ? static_cast<const uint16_t*>(p.bias)[n] : (uint16_t)0;
+  const int64_t m = i / p.N, tile = n / 16;  // K is within one tile and one group
+  float y = 0.f;
+  if (p.K > 0) {
+    const float s = from16<BF16>(static_cast<const uint16_t*>(p.scales)[n]);
+    const int z = p.zeros ? p.zeros[n] : 8;
+    const uint32_t w = p.qw[tile * 256 + 4 * (n % 16)];
+    for (int k = 0; k < p.K; ++k)
+      y += from16<BF16>(static_cast<const uint16_t*>(p.x)[m * p.ldx + k]) *
+           (float)((int)(w >> (4 * (k / 2) + 16 * (k % 2)) & 15) - z);
+    y *= s;
+  }
+  if (p.bias) y += from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]);
+  static_cast<uint16_t*>(p.y)[m * p.ldy + n] = to16<BF16>(y);
 }
 
 // WMAX: the waves of one workgroup, and of all workgroups on a compute unit,
 // that the instance's registers allow.  K is split over as many waves as let
 // all workgroups run at once.
-template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX, bool WIDE>
+template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX>
 hipError_t run(const W4Args& a, hipStream_t s) {
   static_assert(NT <= 4 && WMAX * MT * 4096 <= 160 << 10, "the sums lie where x was");
   const int NB = (a.N + 15) / 16, KB = (a.K + 127) / 128;
@@ -252,46 +266,43 @@ hipError_t run(const W4Args& a, hipStream_t s) {
   int kw = each < WMAX / MW ? WMAX / MW / (int)each : 1;
   if (kw < 4 / MW) kw = 4 / MW;
   if (kw > KB) kw = KB;
-  w4_kernel<BF16, MT, NT, U, PER, R, MW, WMAX, WIDE><<<grid, 64 * kw * MW, kw * MW * MT * 4096, s>>>(a);
+  w4_kernel<BF16, MT, NT, U, PER, R, MW, WMAX><<<grid, 64 * kw * MW, kw * MW * MT * 4096, s>>>(a);
   return hipGetLastError();
 }
 
 template <bool BF16, int PER, int R>
 hipError_t few(const W4Args& a, hipStream_t s) {
   const int NB = (a.N + 15) / 16;
-  if (NB < 1024) return run<BF16, 1, 1, 2, PER, R, 1, 16, true>(a, s);
-  return run<BF16, 1, 2, 2, PER, R, 1, R == 4 || PER == 1 ? 12 : 16, true>(a, s);
+  if (NB < 1024) return run<BF16, 1, 1, 2, PER, R, 1, 16>(a, s);
+  return run<BF16, 1, 2, 2, PER, R, 1, R == 4 || PER == 1 ? 12 : 16>(a, s);
 }
 
 template <bool BF16, int PER>
-hipError_t wide(const W4Args& a, hipStream_t s) {
+hipError_t sized(const W4Args& a, hipStream_t s) {
   const int NB = (a.N + 15) / 16;
   if (a.M <= 4) return few<BF16, PER, 1>(a, s);
   if (a.M <= 8) return few<BF16, PER, 2>(a, s);
   if (a.M <= 16) return few<BF16, PER, 4>(a, s);
   if (a.M <= 32) {
-    if (NB < 512) return run<BF16, 2, 1, 1, PER, 8, 1, 16, true>(a, s);
-    return run<BF16, 2, 2, 1, PER, 8, 1, PER == 1 ? 8 : 12, true>(a, s);
+    if (NB < 512) return run<BF16, 2, 1, 1, PER, 8, 1, 16>(a, s);
+    return run<BF16, 2, 2, 1, PER, 8, 1, PER == 1 ? 8 : 12>(a, s);
   }
-  if (NB < 512) return run<BF16, 2, 1, 1, PER, 8, 2, 16, true>(a, s);
-  if constexpr (PER == 4) return run<BF16, 2, 4, 1, PER, 8, 2, 12, true>(a, s);
-  else return run<BF16, 2, 2, 1, PER, 8, 2, PER == 1 ? 8 : 12, true>(a, s);
+  if (NB < 512) return run<BF16, 2, 1, 1, PER, 8, 2, 16>(a, s);
+  if constexpr (PER == 4) return run<BF16, 2, 4, 1, PER, 8, 2, 8>(a, s);
+  else return run<BF16, 2, 2, 1, PER, 8, 2, PER == 1 ? 8 : 12>(a, s);
 }
 
 template <bool BF16>
 hipError_t pick(const W4Args& a, hipStream_t s) {
-  if (a.K == 0) {
+  if (a.K < 8) {
     const int64_t blocks = ((int64_t)a.M * a.N + 255) / 256;
     if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-    w4_bias_kernel<BF16><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
+    w4_short_kernel<BF16><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
     return hipGetLastError();
   }
-  // 16-byte rows, and tile rows that a 31-bit byte offset reaches
-  if ((reinterpret_cast<uintptr_t>(a.x) & 15) || a.ldx % 8 || a.K % 8 || a.ldx > (1 << 23) || a.K > (1 << 23))
-    return run<BF16, 1, 1, 1, 1, 4, 1, 8, false>(a, s);
-  if (a.group % 128 == 0) return wide<BF16, 4>(a, s);
-  if (a.group % 64 == 0 && 128 % a.group == 0) return wide<BF16, 2>(a, s);
-  return wide<BF16, 1>(a, s);
+  if (a.group % 128 == 0) return sized<BF16, 4>(a, s);
+  if (a.group % 64 == 0 && 128 % a.group == 0) return sized<BF16, 2>(a, s);
+  return sized<BF16, 1>(a, s);
 }
 
 }  // namespace

@@ -73,7 +73,7 @@ int mi_decode_last_hip_error(mi_decode_handle_t h);
  * y[m][n] = round( sum_k x[m][k] * (c[n][k] - z[n][k / group]) * s[n][k / group] + bias[n] )
  * for 0 <= m < M, 0 <= n < N, 0 <= k < K: sums in binary32, one rounding to y's type.
  *   x [M, K] and y [M, N] of type dtype with unit-stride rows ldx >= K and
- *   ldy >= N apart; bias [N] of type dtype or NULL.
+ *   ldy >= N apart (ldx at most 2^25, K at most 2^30); bias [N] of type dtype or NULL.
  *   qweight: the codes c, 0..15, in tiles of 16 rows by 128 columns, 1 KiB
  *   each: tile (n / 16, k / 128) is number (n / 16) * ceil(K / 128) + k / 128.
  *   Its 32-bit word 4 * l + j with l = 16 c + r holds row 16 (n / 16) + r,
