@@ -37,7 +37,7 @@ constexpr int64_t kJoinInside = 192 << 10;
 constexpr int kItem = 16;  // what starting and ending an item costs, in tiles
 
 template <int CODE, int D, int NT>
-__global__ __launch_bounds__(64 * kWaves, NT * D >= 256 ? 1 : 2) void attend_kernel(AttendArgs p, int blocks) {
+__global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kernel(AttendArgs p, int blocks) {
   constexpr int ROWS = 16 * NT, KS = D / 32, DT = D / 16, VW = D / 64;  // VW: 32-bit words of a token's values in a lane
   constexpr int OS = D + 4;
   __shared__ float obuf[kWaves][16][OS];
@@ -487,7 +487,7 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
   const int64_t blocks = (rows + ROWS - 1) / ROWS;
   if (blocks * a.batch.batch > INT32_MAX) return hipErrorInvalidConfiguration;
-  int grid = (NT * D >= 256 ? 1 : 2) * (a.cus < 304 ? a.cus : 304);
+  int grid = (NT * D > 384 ? 1 : 2) * (a.cus < 304 ? a.cus : 304);
   static_assert(sizeof(float) * ROWS * (D + 2) * 2 * 2 * 304 <= MI_DECODE_WORKSPACE_BYTES, "partial results");
   const double tiles = (double)blocks * a.batch.batch * a.cache.kv_heads * (a.max_len / kTile + 1);
   if (tiles < grid) grid = (int)tiles;

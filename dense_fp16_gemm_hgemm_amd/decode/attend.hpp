@@ -105,9 +105,10 @@ __device__ inline Block<TILE> block_of(const AttendArgs& p, int G, int block_row
   if (pair >= pairs) return k;
   const int b = blocks == 1 ? pair : pair / blocks, rb = pair - b * blocks;
   k.b = b;
+  const int held = p.batch.lens[b];  // requested before the tokens' bounds are waited for
   const Span sp = span_of(p.batch, b);
   const int64_t cap = (int64_t)p.batch.table_cols * p.cache.page_size;
-  const int len = (int)min((int64_t)max(p.batch.lens[b], 0), cap);
+  const int len = (int)min((int64_t)max(held, 0), cap);
   k.first = sp.first;
   k.r0 = rb * block_rows;
   const int64_t all = (int64_t)min(sp.n, p.batch.max_tokens) * G;
