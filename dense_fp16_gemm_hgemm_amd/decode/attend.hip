@@ -34,7 +34,8 @@ constexpr int kTile = 32;
 // Parts of an item, in bytes, up to which its last workgroup adds them itself;
 // beyond, a second kernel does.
 constexpr int64_t kJoinInside = 192 << 10;
-constexpr int kItem = 16;  // what starting and ending an item costs, in tiles
+constexpr int kItem = 16;   // what starting and ending an item costs, in tiles
+constexpr int kShort = 16;  // tiles of an item that is not worth cutting
 
 template <int CODE, int D, int NT>
 __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kernel(AttendArgs p, int blocks) {
@@ -55,26 +56,41 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
   // row block `at` + i, and the wave takes its numbers from there
   int at = 0;
   Block<kTile> mine = block_of<kTile>(p, G, ROWS, blocks, lane, pairs);
-  int64_t total = 0;
+  int64_t total = 0, items = 0;
+  int alike = 0;       // not 0: every item has this length on the line
   uint32_t ahead = 0;  // line of the blocks up to the lane's own, for one head
+  int most = 0;        // the most tiles of a block
+  auto length = [&](int tiles) { return (uint32_t)(alike ? alike : tiles + kItem); };
   auto extend = [&]() {
-    ahead = mine.tiles > 0 ? (uint32_t)mine.tiles + kItem : 0u;
+    ahead = mine.tiles > 0 ? length(mine.tiles) : 0u;
+    most = max(most, mine.tiles);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const uint32_t o = (uint32_t)__shfl_up((int)ahead, d);
+      most = max(most, __shfl_xor(most, d));
       if (lane >= d) ahead += o;
     }
     return (uint32_t)lane_value((int)ahead, 63);
   };
   while (true) {
     total += extend();
+    items += __builtin_popcountll(__ballot(mine.tiles > 0));
     if (at + 64 >= pairs) break;
     at += 64;
     mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
   }
-  total *= H;
+  total *= H, items *= H;
+  most = __builtin_amdgcn_readfirstlane(most);
   const int64_t each = (int64_t)((double)total / (double)(int)gridDim.x) + 1;
-  const int chunk = (int)((each + kWaves - 1) / kWaves) * kWaves;
+  int chunk = (int)((each + kWaves - 1) / kWaves) * kWaves;
+  // Items that are short, or not much longer than a piece, are not cut: with
+  // one item to a workgroup nothing is joined (us cut and whole: 64 x 256 tokens
+  // 17.0 and 11.2, 16 x 512 14.6 and 10.4, 1 x 512 9.6 and 10.2).
+  if (items <= (int64_t)gridDim.x && (most <= kShort || 4 * (int64_t)(most + kItem) <= 7 * each)) {
+    alike = chunk = most + kItem;
+    total = items * alike;
+    if (at == 0) extend();
+  }
   const int64_t begin = (int64_t)blockIdx.x * chunk, end = min(begin + chunk, total);
   if (p.join && tid == 0) p.join[blockIdx.x].parts = 0;
   if (begin >= end) return;
@@ -93,9 +109,10 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
   Block<kTile> blk = mine.of_lane(who);
   int h, v0;  // head, and where in the item's line the piece begins
   {
-    const uint32_t off = (uint32_t)(begin - (before + (uint32_t)lane_value((int)ahead, who) - (blk.tiles + kItem)) * H);
-    h = (int)(off / (uint32_t)(blk.tiles + kItem));
-    v0 = (int)(off % (uint32_t)(blk.tiles + kItem));
+    const uint32_t len = length(blk.tiles);
+    const uint32_t off = (uint32_t)(begin - (before + (uint32_t)lane_value((int)ahead, who) - len) * H);
+    h = (int)(off / len);
+    v0 = (int)(off % len);
   }
   int64_t left = end - begin;
 
@@ -463,8 +480,8 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
   };
 
   while (true) {
-    const int v1 = (int)min((int64_t)(blk.tiles + kItem), v0 + left);
-    const int s0 = max(v0 - kItem, 0), s1 = max(v1 - kItem, 0);
+    const int v1 = (int)min((int64_t)length(blk.tiles), v0 + left);
+    const int s0 = max(v0 - kItem, 0), s1 = min(max(v1 - kItem, 0), blk.tiles);
     if (s1 > s0) item(blk, h, s0, s1);
     left -= v1 - v0;
     if (left <= 0) break;

@@ -295,6 +295,9 @@ mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cac
   if ((int64_t)q_heads / cache->kv_heads * (batch->max_tokens > 0 ? batch->max_tokens : 1) > (1 << 24))
     return MI_DECODE_ERR_UNSUPPORTED;
   if (batch->batch == 0 || batch->tokens == 0) return MI_DECODE_OK;
+  // a sequence's heads on the line of work are counted in 32 bits
+  if (((int64_t)batch->table_cols * cache->page_size / 32 + 32) * cache->kv_heads > INT32_MAX)
+    return MI_DECODE_ERR_UNSUPPORTED;
   TRY(check_rows(q, q_heads, cache->head_dim));
   TRY(check_rows(out, q_heads, cache->head_dim));
   if (batch->tokens > 1 && out->token_stride < cache->head_dim) return MI_DECODE_ERR_INVALID_ARG;
