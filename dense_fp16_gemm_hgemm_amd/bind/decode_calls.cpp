@@ -1,10 +1,10 @@
 // The calls of Decode (decode.py) from torch tensors to the C ABI of libmi_decode.
 //
 // A decode step makes many calls of a few microseconds each.  Checks, output
-// and launch from Python with ctypes take 10 (w4_linear) to 22 us (kv_append), longer than the
-// kernels; here they take 5 and 11 us (two launches).  A call returns its result, or the status of a call
-// that the library refused; arguments that do not fit raise ValueError or
-// TypeError.  No C++ exception leaves a function.
+// and launch from Python with ctypes take 10 us (w4_linear) to 22 (kv_append),
+// longer than the kernels; here they take about 5.  A call returns its result,
+// or the status of a call that the library refused; arguments that do not fit
+// raise ValueError or TypeError.  No C++ exception leaves a function.
 #include <cmath>
 
 #include <torch/csrc/autograd/python_variable.h>

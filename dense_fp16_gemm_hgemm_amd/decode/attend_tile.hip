@@ -13,6 +13,11 @@
 // first and multiplies then, so that of the two waves of a SIMD one has vector
 // work while the other has matrix work.
 //
+// Bound: each wave's chain of products, exponentials and conversions, with two
+// waves a SIMD (registers).  2 x 2048 queries of 32 heads against 8192 tokens:
+// 536 us, 900 TFLOP/s; matrix pipes busy 41 % of it.  Products with fragments
+// read just before use 600 us, page numbers and addresses per lane 567.
+//
 // Scales.  A page's value scale would cost a product for each weight; it goes
 // into the exponent instead: x = 2^{z - m + log2 v}, o += x code, l += x / v.
 // Where a scale allows no logarithm the weights are formed one by one.

@@ -183,6 +183,7 @@ mi_decode_status_t mi_decode_kv_read(mi_decode_handle_t h, const mi_decode_cache
  * Query head h reads key-value head h / (q_heads / kv_heads).  A query that
  * sees nothing (p < 0, or no valid page) gives zeros.  What is not seen does
  * not enter the result, whatever its codes and scales are (NaN among them).
+ * A query that sees a NaN code may be NaN in all its channels.
  *   max_len: no lens[b] is larger; used to plan the split of long sequences
  *   over workgroups, not for correctness.
  *   q, out: [tokens][q_heads][head_dim] of type dtype; q_heads a multiple of
