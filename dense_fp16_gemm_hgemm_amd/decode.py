@@ -39,7 +39,11 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmi_decod
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python dense_fp16_gemm_hgemm_amd/build.py`")
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _decode_calls as _calls  # noqa: E402  (needs torch and the library above)
+try:
+    from . import _decode_calls as _calls  # needs torch and the library above
+except ImportError as e:
+    raise ImportError("_decode_calls.so is not built for this Python and torch: run "
+                      "`python dense_fp16_gemm_hgemm_amd/build.py`") from e
 
 MI_DECODE_OK = 0
 MI_DECODE_ERR_INVALID_ARG = 1

@@ -35,9 +35,11 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;
-// Parts of an item, in bytes, up to which its last workgroup adds them itself;
-// beyond, a second kernel does.
-constexpr int64_t kJoinInside = 192 << 10;
+// Bytes of parts that an item may have up to which its last workgroup adds them
+// itself; beyond, a second kernel does.  us inside and beyond: 41 KB (4 x 2048
+// tokens, 8 rows) 14.8 and 15.8, 82 KB (16 rows) 19.1 and 17.0, 147 KB (1 x
+// 8192, 16 rows) 22.1 and 17.6.
+constexpr int64_t kJoinInside = 80 << 10;
 constexpr int kItem = 16;   // what starting and ending an item costs, in tiles
 constexpr int kShort = 16;  // tiles of an item that is not worth cutting
 
@@ -515,8 +517,11 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   static_assert(sizeof(float) * ROWS * (D + 2) * 2 * 2 * 304 <= MI_DECODE_WORKSPACE_BYTES, "partial results");
   const double tiles = (double)blocks * a.batch.batch * a.cache.kv_heads * (a.max_len / kTile + 1);
   if (tiles < grid) grid = (int)tiles;
-  // an item has grid / kv_heads parts at most: a sequence's heads are alike
-  const int64_t part_rows = (grid / a.cache.kv_heads + 1) * (rows < ROWS ? rows : ROWS);
+  // An item has grid / kv_heads parts at most, as a sequence's heads are alike,
+  // and no part but the ends is below 8 tiles, or a sixteenth of 256.
+  const int64_t reach = a.max_len / kTile + 1, cut = reach >= 256 ? 16 : 8;
+  const int64_t by_grid = grid / a.cache.kv_heads + 1, by_len = reach / cut + 2;
+  const int64_t part_rows = (by_grid < by_len ? by_grid : by_len) * (rows < ROWS ? rows : ROWS);
   AttendArgs b = a;
   if (part_rows * D * 4 <= kJoinInside) b.join = nullptr;
   attend_kernel<CODE, D, NT><<<grid, 64 * kWaves, 0, s>>>(b, (int)blocks);
