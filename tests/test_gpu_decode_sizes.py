@@ -126,3 +126,27 @@ def test_append_and_read_many_sequences(d, new):
         # the page's scale is that of its largest new value
         slot = values(take_pages(getattr(cache, which), page_of)).abs().amax((2, 3))
         assert torch.all(slot == 127)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_offsets_past_32_bits_append_read_and_attend(d, new):
+    """Sequences on the last pages of a cache of over 4 GiB a side: 2 rows a token, 80 for 40."""
+    page, H, D = 256, 8, 128
+    pages = 2 ** 32 // (H * page * D) + 40
+    cache = decode.KvCache(*[torch.empty((pages, H, page, D), dtype=torch.int8, device=DEV) for _ in range(2)],
+                           *[torch.full((pages, H), 0.03, device=DEV) for _ in range(2)])
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    rows = [[pages - 1, pages - 4, 0], [pages - 2, 1, pages - 3]]
+    for p in {p for r in rows for p in r}:
+        for x in (cache.k, cache.v):
+            x[p] = random_codes((H, page, D), torch.int8, gen)
+    table, past = put(rows), [600 - new, 513 - new]
+    lens, cu = [n + new for n in past], [0, new, 2 * new]
+    q, k, v = (torch.randn((2 * new, h, D), device=DEV, generator=gen).half() for h in (2 * H, H, H))
+    d.kv_append(cache, k, v, table, put(past), put(cu), new)
+    rk, rv = d.kv_read(cache, table, put(past), put(cu), tokens=2 * new, max_tokens=new)
+    for have, want, scale in ((rk, k, cache.k_scale), (rv, v, cache.v_scale)):
+        step = scale[[p for r in rows for p in r]].max().to(F)
+        assert torch.all((have.to(F) - want.to(F)).abs() <= step * (0.5 + 2.0 ** -20) + half_step(torch.float16) * 8)
+    out = d.kv_attend(q, cache, table, put(lens), put(cu), new, max_len=max(lens))
+    check(out, cache, q, table.cpu(), lens, cu)
