@@ -85,9 +85,11 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   // rows may begin at any element (the hardware takes such loads as they are).
   // Tokens past M read the last one's row and are not stored; a piece that
   // crosses K is read 8 columns before K and shifted, one past K is zero.
+  // Distances are counted in 32 bits, so only to the last of the wave's own
+  // rows (31 rows of 2^25 elements at most), however many rows follow.
   const int xrow = lane >> 4, xcol = lane & 15;
   const uint8_t* xb = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.x) + m0 * p.ldx);
-  const uint32_t last = (uint32_t)(max(p.M - 1 - m0, 0) * p.ldx * 2), x0 = (uint32_t)(xrow * p.ldx * 2), x4 = (uint32_t)(p.ldx * 8);
+  const uint32_t last = (uint32_t)(min(max(p.M - 1 - m0, 0), 16 * MT - 1) * p.ldx * 2), x0 = (uint32_t)(xrow * p.ldx * 2), x4 = (uint32_t)(p.ldx * 8);
   if (m0 >= p.M) xb = static_cast<const uint8_t*>(p.x);
   // the wave's [16 MT][16] pieces; piece q of row i lies at q ^ (i % 16), so
   // that eight rows' pieces of one column do not meet in a bank
