@@ -23,6 +23,8 @@
 // where sum x is one more matrix product, by ones, shared by the NT tiles.
 // Both products are exact in binary32 and the offset at most doubles to
 // quadruples the terms' size, so this costs about two of binary32's 24 bits.
+// Where x is infinite, or the offset takes a sum past binary32, the difference
+// is NaN: a result that is not finite is summed again, term by term.
 #include "device.hpp"
 
 namespace mid {
@@ -52,6 +54,25 @@ __device__ inline u32x4 unpack(uint32_t w, uint32_t base) {
     constexpr uint32_t mask = 0x03c003c0u;
     return u32x4{(w << 6 & mask) | base, (w << 2 & mask) | base, (w >> 2 & mask) | base, (w >> 6 & mask) | base};
   }
+}
+
+// sum_k x[m][k] ((c - z) s), one term after the other.
+template <bool BF16>
+__device__ inline float sum_terms(const W4Args& p, int64_t m, int n) {
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + m * p.ldx;
+  const uint16_t* scales = static_cast<const uint16_t*>(p.scales) + n;
+  const int64_t np = (int64_t)((p.N + 15) >> 4) * 16;
+  const uint32_t* tiles = p.qw + (int64_t)(n >> 4) * ((p.K + 127) >> 7) * 256 + 4 * (n & 15);
+  float y = 0.f;
+  for (int k0 = 0; k0 < p.K; k0 += 8) {  // a word: eight columns of one group
+    const uint32_t w = tiles[(int64_t)(k0 >> 7) * 256 + (k0 >> 3 & 3) * 64 + (k0 >> 5 & 3)];
+    const int64_t at = k0 / p.group * np;
+    const float s = from16<BF16>(scales[at]);
+    const int z = p.zeros ? p.zeros[at + n] : 8;
+    for (int e = 0; e < 8 && k0 + e < p.K; ++e)
+      y = __builtin_fmaf(from16<BF16>(x[k0 + e]), (float)((int)(w >> (4 * (e / 2) + 16 * (e % 2)) & 15) - z) * s, y);
+  }
+  return y;
 }
 
 // MT x NT tiles of 16 tokens by 16 rows of weights to a wave, U blocks of 128
@@ -229,7 +250,10 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int row = blockIdx.y * (16 * MT * MW) + m * 16 + (l >> 4) * 4 + e;
-      if (row < p.M) static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(y[e] + b);
+      if (row >= p.M) continue;
+      float v = y[e];
+      if (!(fabsf(v) < INFINITY)) v = sum_terms<BF16>(p, row, n);
+      static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(v + b);
     }
   }
 }
@@ -240,17 +264,8 @@ __global__ __launch_bounds__(256) void w4_short_kernel(W4Args p) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)p.M * p.N) return;
   const int n = (int)(i % p.N);
-  const int64_t m = i / p.N, tile = n / 16;  // K is within one tile and one group
-  float y = 0.f;
-  if (p.K > 0) {
-    const float s = from16<BF16>(static_cast<const uint16_t*>(p.scales)[n]);
-    const int z = p.zeros ? p.zeros[n] : 8;
-    const uint32_t w = p.qw[tile * 256 + 4 * (n % 16)];
-    for (int k = 0; k < p.K; ++k)
-      y += from16<BF16>(static_cast<const uint16_t*>(p.x)[m * p.ldx + k]) *
-           (float)((int)(w >> (4 * (k / 2) + 16 * (k % 2)) & 15) - z);
-    y *= s;
-  }
+  const int64_t m = i / p.N;
+  float y = sum_terms<BF16>(p, m, n);
   if (p.bias) y += from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]);
   static_cast<uint16_t*>(p.y)[m * p.ldy + n] = to16<BF16>(y);
 }
