@@ -24,7 +24,9 @@
 // Both products are exact in binary32 and the offset at most doubles to
 // quadruples the terms' size, so this costs about two of binary32's 24 bits.
 // Where x is infinite, or the offset takes a sum past binary32, the difference
-// is NaN: a result that is not finite is summed again, term by term.
+// is NaN: a row of a workgroup's results that are not all finite is summed
+// again, term by term, by all its threads (1 x 4096 x 4096 with a NaN 17 us, 64 x 14336 x
+// 4096 with one such row 72; by the thread that has the result 266 and 341).
 #include "device.hpp"
 
 namespace mid {
@@ -56,21 +58,24 @@ __device__ inline u32x4 unpack(uint32_t w, uint32_t base) {
   }
 }
 
-// sum_k x[m][k] ((c - z) s), one term after the other.
+// sum_k x[m][k] ((c - z) s), one term after the other, over every step-th word
+// of eight columns.
 template <bool BF16>
-__device__ inline float sum_terms(const W4Args& p, int64_t m, int n) {
+__device__ inline float sum_terms(const W4Args& p, int64_t m, int n, int first, int step) {
   const uint16_t* x = static_cast<const uint16_t*>(p.x) + m * p.ldx;
   const uint16_t* scales = static_cast<const uint16_t*>(p.scales) + n;
   const int64_t np = (int64_t)((p.N + 15) >> 4) * 16;
   const uint32_t* tiles = p.qw + (int64_t)(n >> 4) * ((p.K + 127) >> 7) * 256 + 4 * (n & 15);
   float y = 0.f;
-  for (int k0 = 0; k0 < p.K; k0 += 8) {  // a word: eight columns of one group
+  for (int k0 = 8 * first; k0 < p.K; k0 += 8 * step) {
     const uint32_t w = tiles[(int64_t)(k0 >> 7) * 256 + (k0 >> 3 & 3) * 64 + (k0 >> 5 & 3)];
     const int64_t at = k0 / p.group * np;
     const float s = from16<BF16>(scales[at]);
     const int z = p.zeros ? p.zeros[at + n] : 8;
-    for (int e = 0; e < 8 && k0 + e < p.K; ++e)
-      y = __builtin_fmaf(from16<BF16>(x[k0 + e]), (float)((int)(w >> (4 * (e / 2) + 16 * (e % 2)) & 15) - z) * s, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k0 + e < p.K)
+        y = __builtin_fmaf(from16<BF16>(x[k0 + e]), (float)((int)(w >> (4 * (e / 2) + 16 * (e % 2)) & 15) - z) * s, y);
   }
   return y;
 }
@@ -89,7 +94,7 @@ __device__ inline float sum_terms(const W4Args& p, int64_t m, int n) {
 template <bool BF16, int MT, int NT, int U, int PER, int R, int MW, int WMAX>
 __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   constexpr int FL = 4 / PER;  // group sums to a block
-  extern __shared__ float red[];
+  extern __shared__ __attribute__((aligned(16))) float red[];
   const int lane = threadIdx.x & 63, KW = (int)(blockDim.x >> 6) / MW;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave / MW, mw = wave % MW;
@@ -233,11 +238,29 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   // red[kw][mw][m][t][lane] as 4 tokens each; summed in the order of kw
   constexpr int PART = MT * NT * 64;
   f32x4* part = reinterpret_cast<f32x4*>(red);
+  __shared__ uint32_t again[2];  // rows of the workgroup, 64 at most, with a sum that is not finite
+  if (threadIdx.x < 2) again[threadIdx.x] = 0;
   __syncthreads();  // every wave is done with its piece
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t) part[wave * PART + (m * NT + t) * 64 + lane] = total[m][t];
+  float odd = 0.f;  // NaN if one of the lane's sums is not finite; scales past N may be anything
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) odd = __builtin_fmaf((nb0 + t) * 16 + r < p.N ? total[m][t][e] : 0.f, 0.f, odd);
+  if (odd != 0.f) {
+    for (int m = 0; m < MT; ++m)
+      for (int e = 0; e < 4; ++e) {
+        const int at = (mw * MT + m) * 16 + c * 4 + e;
+        bool bad = false;
+        for (int t = 0; t < NT; ++t) bad |= (nb0 + t) * 16 + r < p.N && !(fabsf(total[m][t][e]) < INFINITY);
+        if (bad) atomicOr(&again[at >> 5], 1u << (at & 31));
+      }
+  }
   __syncthreads();
   // thread -> (mw, m, t, l): lanes of 16 neighbours hold 16 neighbouring columns of four tokens
   for (int i = threadIdx.x; i < MW * PART; i += blockDim.x) {
@@ -250,12 +273,27 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int row = blockIdx.y * (16 * MT * MW) + m * 16 + (l >> 4) * 4 + e;
-      if (row >= p.M) continue;
-      float v = y[e];
-      if (!(fabsf(v) < INFINITY)) v = sum_terms<BF16>(p, row, n);
-      static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(v + b);
+      if (row < p.M) static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(y[e] + b);
     }
   }
+  if ((again[0] | again[1]) == 0) return;
+  __syncthreads();
+  constexpr int COLS = 16 * NT;
+  const int tid = threadIdx.x, n = nb0 * 16 + tid % COLS;
+  for (int half = 0; half < 2; ++half)
+    for (uint32_t left = again[half]; left; left &= left - 1) {
+      const int64_t row = blockIdx.y * (16 * MT * MW) + 32 * half + __builtin_ctz(left);
+      if (row >= p.M) break;  // the last row of x once more
+      red[tid] = n < p.N ? sum_terms<BF16>(p, row, n, tid / COLS, blockDim.x / COLS) : 0.f;
+      __syncthreads();
+      if (tid < COLS && n < p.N) {
+        float y = red[tid];
+        for (int i = tid + COLS; i < (int)blockDim.x; i += COLS) y += red[i];
+        if (p.bias) y += from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]);
+        static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(y);
+      }
+      __syncthreads();
+    }
 }
 
 // K below 8, where no whole piece of a row exists: one result to a thread.
@@ -265,7 +303,7 @@ __global__ __launch_bounds__(256) void w4_short_kernel(W4Args p) {
   if (i >= (int64_t)p.M * p.N) return;
   const int n = (int)(i % p.N);
   const int64_t m = i / p.N;
-  float y = sum_terms<BF16>(p, m, n);
+  float y = sum_terms<BF16>(p, m, n, 0, 1);
   if (p.bias) y += from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]);
   static_cast<uint16_t*>(p.y)[m * p.ldy + n] = to16<BF16>(y);
 }
