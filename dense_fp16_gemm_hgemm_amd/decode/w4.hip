@@ -25,8 +25,9 @@
 // quadruples the terms' size, so this costs about two of binary32's 24 bits.
 // Where x is infinite, or the offset takes a sum past binary32, the difference
 // is NaN: a row of a workgroup's results that are not all finite is summed
-// again, term by term, by all its threads (1 x 4096 x 4096 with a NaN 17 us, 64 x 14336 x
-// 4096 with one such row 72; by the thread that has the result 266 and 341).
+// again, term by term, by all its threads (1 x 4096 x 4096 with a NaN 17 us, 64
+// x 14336 x 4096 with one such row 72; by the thread that has the result 266
+// and 341).
 #include "device.hpp"
 
 namespace mid {
@@ -56,6 +57,14 @@ __device__ inline u32x4 unpack(uint32_t w, uint32_t base) {
     constexpr uint32_t mask = 0x03c003c0u;
     return u32x4{(w << 6 & mask) | base, (w << 2 & mask) | base, (w >> 2 & mask) | base, (w >> 6 & mask) | base};
   }
+}
+
+// Orders a wave's accesses to its piece of shared memory: what its lanes stored
+// before is what they load after, and the other way round.  The hardware keeps
+// a wave's order; this keeps the compiler's, and costs no instruction.
+__device__ inline void wave_shared() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // sum_k x[m][k] ((c - z) s), one term after the other, over every step-th word
@@ -192,11 +201,13 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
       }
 #pragma unroll
       for (int i = 0; i < R; ++i) xs[(4 * i + xrow) * 16 + (xcol ^ ((4 * i + xrow) & 15))] = xq[u][i];
+      wave_shared();
       u32x4 xf[4][MT];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int m = 0; m < MT; ++m) xf[j][m] = xs[(16 * m + r) * 16 + ((4 * j + c) ^ r)];
+      wave_shared();
       u32x4 w[NT];
       float sc[FL][NT], of[FL][NT];
 #pragma unroll
