@@ -1,6 +1,10 @@
 // Attention over the paged 8-bit cache, one pass over keys and values with the
-// running maximum m and sum l of a softmax (base 2):
-//   m' = max(m, z),  l' = l 2^{m-m'} + sum 2^{z-m'},  o' = o 2^{m-m'} + sum 2^{z-m'} v.
+// running maximum m and sum l of a softmax (base 2), a page's value scale v in
+// the exponent: y = z + log2 v,
+//   m' = max(m, y),  l' = l 2^{m-m'} + sum 2^{y-m'} / v,  o' = o 2^{m-m'} + sum 2^{y-m'} code.
+// Weights become binary16 operands in a unit of the row's own then, whatever
+// other rows see (a unit for the workgroup, the largest scale of its pages,
+// lost rows that do not see that page).
 //
 // Rows.  The G query heads of a key-value head and a sequence's n query tokens
 // are one matrix of G n rows (row r: token r / G, head r % G) against the same
@@ -149,7 +153,8 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
 
     // pages and scales of the wave's next 64 tiles, one to a lane, for each half of a tile
     int pg[2];
-    float ks[2], vr[2], vmax = 0.f;
+    float ks[2], vlog[2];
+    uint64_t plain, odd;  // tiles: all of whose pages exist and have scales that are their logarithm, and that have another
     auto pages = [&](int tile) {
       const int t = tile + kWaves * lane;
 #pragma unroll
@@ -167,31 +172,24 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     auto scales = [&]() {
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        ks[st] = 0.f, vr[st] = 0.f;
+        ks[st] = 0.f, vlog[st] = 0.f;
         if (pg[st] >= 0) {
           const int64_t at = (int64_t)pg[st] * H + h;
           ks[st] = p.cache.k_scale[at];
-          vr[st] = p.cache.v_scale[at];
+          vlog[st] = p.cache.v_scale[at];
         }
       }
     };
-    // Sums are kept in units of the largest value scale so far, and vr becomes
-    // the scales in that unit; one that is not finite reaches the rows that see
-    // it and no others.  Returns what sums in the old unit are multiplied by.
-    auto unit = [&]() {
-      float top = 0.f;
+    // once the scales are there: not before the first tile is requested
+    auto logarithms = [&]() {
+      odd = 0;
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        const float a = fabsf(vr[st]);
-        if (a < INFINITY) top = fmaxf(top, a);
+        const ValueScale vs = value_scale(vlog[st]);
+        vlog[st] = vs.log;
+        odd |= __ballot(pg[st] >= 0 && vs.rest != 1.f);
       }
-#pragma unroll
-      for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-      float down = 1.f;
-      if (top > vmax) down = vmax / top, vmax = top;
-      const float u = vmax > 0.f ? vmax : 1.f;
-      vr[0] /= u, vr[1] /= u;
-      return down;
+      plain = __ballot(pg[0] >= 0 && pg[1] >= 0) & ~odd;
     };
 
     u32x4 kraw[2][KS / 2];
@@ -286,13 +284,23 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
       for (int d = 0; d < DT; ++d) o[nt][d] = f32x4{0, 0, 0, 0};
     }
 
-    unit();
+    logarithms();
     for (; tile < s1; tile += kWaves) {
       const int tok0 = blk.token(tile);
-      const int pg0 = lane_value(pg[0], i), pg1 = lane_value(pg[1], i);
       const float ks0 = lane_value(ks[0], i), ks1 = lane_value(ks[1], i);
-      float vr0 = lane_value(vr[0], i), vr1 = lane_value(vr[1], i);
-      const bool whole = pg0 >= 0 && pg1 >= 0 && tok0 + kTile - 1 <= blk.plo &&
+      const float log0 = lane_value(vlog[0], i), log1 = lane_value(vlog[1], i);
+      const float inv0 = inverse(log0), inv1 = inverse(log1);
+      const bool is_plain = plain >> i & 1;
+      int pg0 = 0, pg1 = 0;
+      float rest0 = 1.f, rest1 = 1.f;
+      if (!is_plain) {
+        pg0 = lane_value(pg[0], i), pg1 = lane_value(pg[1], i);
+        if (odd >> i & 1) {  // read once more: kept, it would take registers from all tiles
+          if (pg0 >= 0) rest0 = value_scale(p.cache.v_scale[(int64_t)pg0 * H + h]).rest;
+          if (pg1 >= 0) rest1 = value_scale(p.cache.v_scale[(int64_t)pg1 * H + h]).rest;
+        }
+      }
+      const bool whole = is_plain && tok0 + kTile - 1 <= blk.plo &&
                          (p.window == 0 || tok0 > blk.phi - p.window || tok0 + kTile - 1 < p.sinks);
       // whether a query at `at` sees the lane's token c: constants against
       // numbers of the tile, which otherwise stay in registers as tokens
@@ -306,12 +314,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
         i = 0;
         pages(next);
         scales();
-        const float down = unit();
-        vr0 *= down, vr1 *= down;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[nt][d] *= down;
+        logarithms();
       }
 
       f32x4 z[NT][2];
@@ -343,7 +346,10 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
       for (int nt = 0; nt < NT; ++nt) {
         const float f0 = fac[nt] * ks0, f1 = fac[nt] * ks1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[nt][0][e] *= f0, z[nt][1][e] *= f1;
+        for (int e = 0; e < 4; ++e) {
+          z[nt][0][e] = __builtin_fmaf(z[nt][0][e], f0, log0);
+          z[nt][1][e] = __builtin_fmaf(z[nt][1][e], f1, log1);
+        }
         if (!whole) {
 #pragma unroll
           for (int st = 0; st < 2; ++st)
@@ -364,15 +370,17 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
         }
         const float base = m[nt] == -INFINITY ? 0.f : m[nt];
 #pragma unroll
-        for (int st = 0; st < 2; ++st)
+        for (int st = 0; st < 2; ++st) {
+          float sum = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float w = __builtin_amdgcn_exp2f(z[nt][st][e] - base);
-            l[nt] += w;
-            float x = w * (st ? vr1 : vr0);
-            if (!whole && z[nt][st][e] == -INFINITY) x = 0.f;
-            pf[nt][4 * st + e] = (_Float16)x;
+            float w = __builtin_amdgcn_exp2f(z[nt][st][e] - base);
+            sum += w;
+            if (!whole) w = z[nt][st][e] == -INFINITY ? 0.f : w * (st ? rest1 : rest0);
+            pf[nt][4 * st + e] = (_Float16)w;
           }
+          l[nt] = __builtin_fmaf(sum, st ? inv1 : inv0, l[nt]);
+        }
       }
 
       if (CODE == MI_DECODE_E4M3 && !whole) {
@@ -442,8 +450,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
           f32x4 x;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            x[y] = o[nt][d + y][e] * vmax;
-            if (CODE == MI_DECODE_INT8) x[y] *= 1.f / kTiny;
+            x[y] = o[nt][d + y][e] * kUnit<CODE>;
           }
           *reinterpret_cast<f32x4*>(&obuf[wave][c][(4 * g + e) * DT + d]) = x;
         }

@@ -33,6 +33,24 @@ __device__ inline float lane_value(float x, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
+// A page's value scale as 2^log times rest.  rest is 1 for scales of at least
+// 2^-80; smaller ones count as 2^-80 (no logarithm for 0, and no weight that
+// leaves binary32), and it has the sign and whatever is not finite.
+struct ValueScale {
+  float log, rest;
+};
+__device__ inline ValueScale value_scale(float v) {
+  const bool finite = fabsf(v) < INFINITY, small = fabsf(v) < 0x1p-80f;
+  return {small ? -80.f : finite ? __builtin_amdgcn_logf(fabsf(v)) : 0.f,
+          small ? v * 0x1p80f : finite ? copysignf(1.f, v) : v};
+}
+// 2^10 / 2^log: sums of weights are in units of 2^-10, which keeps them within
+// binary32 for scales from 2^-80 (and a million tokens) to 2^128.
+__device__ inline float inverse(float log) { return __builtin_amdgcn_exp2f(10.f - log); }
+// What a sum of weights times codes is multiplied by, to go over such a sum of weights.
+template <int CODE>
+constexpr float kUnit = CODE == MI_DECODE_INT8 ? 0x1p10f / kTiny : 0x1p10f;
+
 // Two bytes code + 128 in 16-bit slots as two numbers code 2^-24.
 __device__ inline uint32_t centred(uint32_t w) {
   const _Float16 off = (_Float16)(-128.f * kTiny);

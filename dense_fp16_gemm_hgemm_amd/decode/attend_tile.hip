@@ -18,9 +18,8 @@
 // 536 us, 900 TFLOP/s; matrix pipes busy 41 % of it.  Products with fragments
 // read just before use 600 us, page numbers and addresses per lane 567.
 //
-// Scales.  A page's value scale would cost a product for each weight; it goes
-// into the exponent instead: x = 2^{z - m + log2 v}, o += x code, l += x / v.
-// Where a scale allows no logarithm the weights are formed one by one.
+// Scales.  A page's value scale goes into the exponent here too, and the sum of
+// weights takes it out again once for 8 of them.
 #include "attend.hpp"
 
 namespace mid {
@@ -29,7 +28,7 @@ namespace {
 constexpr int kStage = 64;
 
 // What a stage's buffer says of one of its four 16-token parts.
-struct Part {
+struct alignas(16) Part {
   float ks, vs;  // scales of its page, 0 where there is none
   int page;      // the page, or -1
 };
@@ -244,7 +243,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   entries(s0 + 2);
   __syncthreads();
 
-  float m = -INFINITY, l = 0.f, vmax = 0.f, log_vmax = 0.f;
+  float m = -INFINITY, l = 0.f;
   f32x16 o[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) o[d] = f32x16{};
@@ -283,23 +282,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
       }
     // operands are read six products ahead of their use
     schedule_reads<2 * KS, 6>();
-    // Sums are in units of the largest finite value scale so far.
-    const bool finite = fabsf(mine.vs) < INFINITY;
-    if (__any(finite && fabsf(mine.vs) > vmax)) {
-      float top = finite ? fabsf(mine.vs) : 0.f;
-      top = fmaxf(top, __shfl_xor(top, 1));
-      top = fmaxf(top, __shfl_xor(top, 2));
-      rescale(vmax / top);
-      vmax = top;
-      log_vmax = __builtin_amdgcn_logf(top);
-    }
+    const ValueScale vs = value_scale(mine.vs);
+    const float inv = inverse(vs.log);
     // Token c after the lane's first one (constants, compared with numbers of
     // the stage: left as tokens, 32 of them would stay in registers).
     const int upto = pos - t0 - 4 * hi, after = p.window ? upto - p.window : -1, sink = p.sinks - t0 - 4 * hi;
     auto seen = [&](int c) { return c <= upto && (c > after || c < sink); };
     const int valid = __ballot(mine.page >= 0) & 15;
-    // scales that have a logarithm, and a reciprocal in the unit
-    const bool plain = mine.vs >= 0x1p-126f && mine.vs >= vmax * 0x1p-64f && mine.vs < INFINITY && mine.ks >= 0.f && mine.ks < INFINITY;
+    const bool plain = vs.rest == 1.f && mine.ks >= 0.f && mine.ks < INFINITY;
     const bool whole = valid == 15 && __all(plain) && t0 + kStage - 1 <= wlo &&
                        (p.window == 0 || t0 > whi - p.window || t0 + kStage - 1 < p.sinks);
     float f[4];
@@ -312,18 +302,20 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
         float t = z[i / 2][8 * (i % 2)];
 #pragma unroll
         for (int e = 1; e < 8; ++e) t = fmaxf(t, z[i / 2][8 * (i % 2) + e]);
-        top = fmaxf(top, t * f[i]);
+        top = fmaxf(top, __builtin_fmaf(t, f[i], lane_value(vs.log, i)));
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const float lv = lane_value(vs.log, i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const bool ok = (valid >> i & 1) && seen(16 * i + 8 * (e / 4) + e % 4);
-          const float y = ok ? z[i / 2][8 * (i % 2) + e] * f[i] : -INFINITY;
+          const float y = ok ? __builtin_fmaf(z[i / 2][8 * (i % 2) + e], f[i], lv) : -INFINITY;
           z[i / 2][8 * (i % 2) + e] = y;
           top = fmaxf(top, y);
         }
+      }
     }
     // m moves only when weights would pass 2^8, which binary16 holds as well as 1
     if (__any(top > m + 8.f)) {
@@ -336,10 +328,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     h8 pf[4];
     if (whole) {
       __builtin_amdgcn_sched_barrier(0);
-      const float lv = __builtin_amdgcn_logf(mine.vs) - log_vmax, iv = vmax * __builtin_amdgcn_rcpf(mine.vs);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float c = lane_value(lv, i) - m;
+        const float c = lane_value(vs.log, i) - m;
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -347,18 +338,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
           sum += w;
           pf[i][e] = (_Float16)w;
         }
-        l = __builtin_fmaf(sum, lane_value(iv, i), l);
+        l = __builtin_fmaf(sum, lane_value(inv, i), l);
       }
     } else {
-      const float base = m == -INFINITY ? 0.f : m, vr = mine.vs / (vmax > 0.f ? vmax : 1.f);
+      const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float v = lane_value(vr, i);
+        const float iv = lane_value(inv, i), rest = lane_value(vs.rest, i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float y = z[i / 2][8 * (i % 2) + e], w = __builtin_amdgcn_exp2f(y - base);
-          l += w;
-          pf[i][e] = y == -INFINITY ? (_Float16)0 : (_Float16)(w * v);
+          l = __builtin_fmaf(w, iv, l);
+          pf[i][e] = y == -INFINITY ? (_Float16)0 : (_Float16)(w * rest);
         }
       }
     }
@@ -402,8 +393,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
 
   // o as rows: lane (col, hi) holds channels 32 d + 8 a + 4 hi + 0..3 of row col
   l += __shfl_xor(l, 32);
-  float unit = vmax;
-  if (CODE == MI_DECODE_INT8) unit *= 1.f / kTiny;
+  constexpr float unit = kUnit<CODE>;
   if (parts == 1) {
     if (in)
 #pragma unroll

@@ -1,0 +1,99 @@
+"""Attention over the paged 8-bit cache at the ends of what its arguments may hold: scales, weights
+and query channels of very different sizes, infinities."""
+import math
+
+import pytest
+import torch
+
+from decode_ref import F, QMAX, cached, half_step, layout
+
+pytestmark = pytest.mark.gpu
+decode = pytest.importorskip("dense_fp16_gemm_hgemm_amd.decode")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+from test_gpu_decode_attend import CODES, DEV, TYPES, make, put  # noqa: E402
+
+# query heads of the one key-value head, and new tokens, that reach each attention kernel
+ROWS = [(64, 8, 1), (128, 8, 1), (128, 8, 6), (128, 8, 20), (64, 4, 90), (256, 2, 300)]
+
+
+@pytest.fixture(scope="module")
+def d():
+    h = decode.Decode()
+    yield h
+    h.close()
+
+
+def attend(q, cache, table, lens, cu):
+    """(out, bound) in float64, one query head after the other, each row by the tokens that it sees.
+
+    A kernel rounds a weight times its page's value scale to binary16: half a step, 2^-11 of it, or
+    2^-25 of the largest such product of the row.  Logits carry a dot product's rounding in binary32,
+    2 (D + 8) 2^-24 of its terms' sizes, and exponents of up to 128 one of 2^-17."""
+    D, G, table = cache.head_dim, q.shape[1] // cache.kv_heads, table.to(DEV)
+    out = torch.zeros(q.shape, dtype=F, device=DEV)
+    bound = torch.zeros_like(out)
+    for b in range(len(lens)):
+        n, L = cu[b + 1] - cu[b], lens[b]
+        k, _ = cached(cache, table, b, L, "k")
+        v, _ = cached(cache, table, b, L, "v")
+        page = table[b, torch.arange(L, device=DEV) // cache.page_size].long()
+        seen = torch.arange(L, device=DEV)[None] <= torch.arange(n, device=DEV)[:, None] + (L - n)
+        for h in range(q.shape[1]):
+            x, kh, vh = q[cu[b]:cu[b + 1], h].to(F), k[h // G], v[h // G]
+            z = (x @ kh.t() * D ** -0.5).masked_fill(~seen, -math.inf)
+            size = (x.abs() @ kh.abs().t() * D ** -0.5).masked_fill(~seen, 0).amax(1, keepdim=True)
+            w = torch.softmax(z, -1)
+            most = (w * cache.v_scale[page, h // G].to(F)).amax(1, keepdim=True) * QMAX[cache.v.dtype]
+            out[cu[b]:cu[b + 1], h] = w @ vh
+            bound[cu[b]:cu[b + 1], h] = ((2.0 ** -11 + 2.0 ** -17 + 2 * size * (D + 8) * 2.0 ** -24) * (w @ vh.abs())
+                                         + seen.sum(1, keepdim=True) * 2.0 ** -25 * most)
+    return out, bound
+
+
+def check(got, ref, bound):
+    u, fine = half_step(got.dtype), torch.finfo(got.dtype)
+    err, tol = (got.to(F) - ref).abs(), u * (ref.abs() + bound) + bound + fine.tiny * fine.eps
+    assert torch.isfinite(got).all()
+    assert torch.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("factor", [2.0 ** 18, 1e12])
+@pytest.mark.parametrize("D, G, new", [r for r in ROWS if r[2] > 1])
+def test_a_large_scale_on_a_page_that_only_later_rows_see(d, D, G, new, factor, codes):
+    lens, page = [400 + new], 16
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], torch.bfloat16, 31)
+    cache.v_scale[int(table[0, (lens[0] - 1) // page])] *= factor
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    check(got, *attend(q, cache, table, lens, cu))
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("D, G, new", ROWS)
+def test_scales_far_apart_with_weights_to_match(d, D, G, new, codes):
+    """Pages whose values are 2^20 times larger, with weights 2^20 times smaller: both halves of a sum count."""
+    lens, page = [800 + new], 16
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], torch.bfloat16, 33, spread=0)
+    small = table[0, :25].long().to(DEV)
+    for p in range(25):  # keys of these pages are one direction, in which queries have size
+        cache.k.view(torch.uint8)[int(table[0, p])] = 0
+        cache.k.view(torch.uint8)[int(table[0, p]), :, :, 0] = 127 if codes == "int8" else 0x7e  # QMAX
+    cache.k_scale[small] = 1.0 / QMAX[cache.k.dtype]
+    q[:, :, 0] = 20 * math.log(2) * D ** 0.5  # 2^20 times the weight of a logit of 0
+    cache.v_scale[small] *= 2.0 ** -20
+    rest = table[0, 25:-(-lens[0] // page)].long().to(DEV)
+    cache.k.view(torch.uint8)[rest, :, :, 0] = 0
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    check(got, *attend(q, cache, table, lens, cu))
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("size", [1e-24, 1e-12, 1e30])
+@pytest.mark.parametrize("D, G, new", ROWS)
+def test_very_small_and_very_large_values(d, D, G, new, size, codes):
+    lens, page = [300 + new], 32
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], torch.bfloat16, 35)
+    cache.v_scale.mul_(size)
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    check(got, *attend(q, cache, table, lens, cu))
