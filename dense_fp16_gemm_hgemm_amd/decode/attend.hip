@@ -359,9 +359,9 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
         }
         float top = fmaxf(fmaxf(fmaxf(z[nt][0][0], z[nt][0][1]), fmaxf(z[nt][0][2], z[nt][0][3])),
                           fmaxf(fmaxf(z[nt][1][0], z[nt][1][1]), fmaxf(z[nt][1][2], z[nt][1][3])));
-        // m moves only when weights would pass 2^8, which binary16 holds as well as 1
-        if (__any(top > m[nt] + 8.f)) {
-          const float m1 = fmaxf(m[nt], max16(top));
+        // m is 12 below the largest y and moves when weights would pass 2^15
+        if (__any(top > m[nt] + kMost)) {
+          const float m1 = fmaxf(m[nt], max16(top) - kBelow);
           const float down = m[nt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[nt] - m1);
           m[nt] = m1;
           l[nt] *= down;

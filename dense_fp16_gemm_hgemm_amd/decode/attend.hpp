@@ -10,6 +10,12 @@ namespace {
 constexpr int kRsrcWord3 = 0x00020000;
 constexpr int kDeviceScope = 16;  // cache policy SC1
 constexpr float kTiny = 0x1p-24f;  // int8 codes as operands are in units of this
+// Weights as operands go up to binary16's upper end: m is kept kBelow under the
+// largest exponent that it was set by, and set again when a weight would pass
+// 2^kMost.  So weights down to 2^-26 of the largest have all 11 bits and vanish
+// below 2^-37 (a long flat context beside one dominant token: with weights of
+// at most 1, those below 2^-14 lost bits and those below 2^-25 everything).
+constexpr float kBelow = 12.f, kMost = 15.f;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ inline f32x16 mma(h8 a, h8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }

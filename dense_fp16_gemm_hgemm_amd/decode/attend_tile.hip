@@ -317,9 +317,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
         }
       }
     }
-    // m moves only when weights would pass 2^8, which binary16 holds as well as 1
-    if (__any(top > m + 8.f)) {
-      const float m1 = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+    // m is 12 below the largest y and moves when weights would pass 2^15
+    if (__any(top > m + kMost)) {
+      const float m1 = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) - kBelow);
       const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - m1);
       m = m1;
       l *= by;

@@ -97,3 +97,32 @@ def test_very_small_and_very_large_values(d, D, G, new, size, codes):
     cache.v_scale.mul_(size)
     got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
     check(got, *attend(q, cache, table, lens, cu))
+
+
+@pytest.mark.parametrize("share", [0.01, 0.003])
+@pytest.mark.parametrize("D, G, new, batch", [(64, 8, 1, 600), (128, 1, 1, 1), (128, 8, 6, 600), (128, 8, 20, 1), (256, 2, 300, 1)])
+def test_a_dominant_token_over_a_long_flat_rest(d, D, G, new, batch, share):
+    """One token with a value of zero has nearly all the weight; the result is what the others share.
+    Sequences of a large batch, which all have the same pages here, are not cut into parts."""
+    L, page = 131072 + new, 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    pages = -(-L // page)
+    table = layout([L], page, pages, torch.Generator().manual_seed(6)).to(DEV)
+    cache = decode.KvCache.empty(pages, 1, D, page)
+    cache.v.copy_(torch.randint(32, 128, cache.v.shape, generator=g, device=DEV, dtype=torch.int8))
+    cache.v_scale.fill_(1.0)
+    cache.k_scale.fill_(1.0 / 127)
+    first = int(table[0, 0])
+    cache.k[first, 0, 0, 0] = 127
+    cache.v[first, 0, 0] = 0
+    q = torch.zeros((batch * new, G, D), device=DEV)
+    q[:, :, 0] = math.log(131072 * (1 - share) / share) * D ** 0.5
+    q = q.bfloat16()
+    cu = torch.arange(batch + 1, dtype=torch.int32, device=DEV) * new
+    got = d.kv_attend(q, cache, table.repeat(batch, 1), put([L] * batch), cu, new, max_len=L)
+    logit = q[0, 0, 0].to(F) * D ** -0.5
+    v = cache.v[table[0].long(), 0].view(-1, D)[:L].to(F)
+    sums, count = v.cumsum(0)[L - new:], torch.arange(L - new, L, device=DEV, dtype=F)  # the others that a row sees
+    ref = (sums / (count + logit.exp())[:, None])[:, None].expand(new, G, D).repeat(batch, 1, 1)
+    # a weight's half step, and the dominant logit's rounding (its one term of D, in binary32)
+    check(got, ref, (2.0 ** -11 + 2.0 ** -17 + 2 * logit * (D + 8) * 2.0 ** -24) * ref)
