@@ -238,7 +238,6 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     int pos[NT];
     __syncthreads();  // the last item's reads of shared memory are over
     {
-      // the row's largest magnitude goes to [1, 2): bf16 keeps all its bits in binary16
       float x[KS][8], top = 0.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
@@ -249,8 +248,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
           top = fmaxf(top, fabsf(x[s][e]));
         }
       top = max16(top);
-      const int ex = top > 0.f && top < INFINITY ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) : 127;
-      const float down = __builtin_bit_cast(float, (uint32_t)min(max(254 - ex, 1), 254) << 23);
+      const float down = p.bf16 ? query_unit(top) : 1.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         h8 f;

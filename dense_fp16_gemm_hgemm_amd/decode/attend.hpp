@@ -39,6 +39,14 @@ __device__ inline float lane_value(float x, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
+// What a row of bf16 queries is multiplied by to become binary16: its largest
+// magnitude goes to [2^15, 2^16).  Channels down to 2^-32 of that one keep their
+// 8 bits then, and they vanish below 2^-40.  binary16 queries stay as they are.
+__device__ inline float query_unit(float top) {
+  const int ex = top > 0.f && top < INFINITY ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) : 142;
+  return __builtin_bit_cast(float, (uint32_t)min(269 - ex, 254) << 23);
+}
+
 // A page's value scale as 2^log times rest.  rest is 1 for scales of at least
 // 2^-80; smaller ones count as 2^-80 (no logarithm for 0, and no weight that
 // leaves binary32), and it has the sign and whatever is not finite.

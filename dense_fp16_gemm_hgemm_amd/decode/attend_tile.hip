@@ -190,8 +190,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     }
   };
 
-  // the wave's queries: rows as columns of the right operand, the largest
-  // magnitude in [1, 2), with the scale's sign
+  // the wave's queries: rows as columns of the right operand, with the scale's sign
   const int row = 32 * wave + col;
   const bool in = row < blk.rows;
   const int pos = in ? blk.start + (blk.r0 + row) / G : -1;
@@ -223,8 +222,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(s, e)));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const int ex = top > 0.f && top < INFINITY ? (int)(__builtin_bit_cast(uint32_t, top) >> 23) : 127;
-    const float down = __builtin_bit_cast(float, (uint32_t)min(max(254 - ex, 1), 254) << 23);
+    const float down = p.bf16 ? query_unit(top) : 1.f;
     const float by = p.scale < 0.f ? -down : down;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

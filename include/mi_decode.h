@@ -188,9 +188,11 @@ mi_decode_status_t mi_decode_kv_read(mi_decode_handle_t h, const mi_decode_cache
  *   over workgroups, not for correctness.
  *   q, out: [tokens][q_heads][head_dim] of type dtype; q_heads a multiple of
  *   kv_heads.  out must not overlap an input.
- * Products take the queries in 11 significant bits (bf16: exact up to a scale
- * by a power of two per row), codes exactly, and softmax weights rounded to
- * binary16; sums and statistics are binary32.
+ * Products take codes and binary16 queries exactly, bf16 queries too down to
+ * 2^-32 of their row's largest channel (below, as a multiple of 2^-39 of it;
+ * nothing below 2^-40), and softmax weights times their page's value scale in
+ * 11 significant bits down to 2^-26 of the row's largest (below, as a multiple
+ * of 2^-36 of it; nothing below 2^-37).  Sums and statistics are binary32.
  */
 mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cache_t* cache,
                                        mi_decode_dtype_t dtype, const mi_decode_batch_t* batch,

@@ -126,3 +126,18 @@ def test_a_dominant_token_over_a_long_flat_rest(d, D, G, new, batch, share):
     ref = (sums / (count + logit.exp())[:, None])[:, None].expand(new, G, D).repeat(batch, 1, 1)
     # a weight's half step, and the dominant logit's rounding (its one term of D, in binary32)
     check(got, ref, (2.0 ** -11 + 2.0 ** -17 + 2 * logit * (D + 8) * 2.0 ** -24) * ref)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("D, G, new", ROWS)
+def test_queries_of_very_different_channels(d, D, G, new, codes, dtype):
+    """A channel of 60000 that meets zeros beside channels of a thousandth that decide."""
+    lens, page = [500 + new], 32
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], TYPES[dtype], 41)
+    cache.k.view(torch.uint8)[..., 0] = 0
+    cache.k_scale.mul_(300.0)
+    q.mul_(1.0 / 300)
+    q[:, :, 0] = 60000.0
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    check(got, *attend(q, cache, table, lens, cu))
