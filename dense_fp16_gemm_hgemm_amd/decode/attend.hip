@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     // pages and scales of the wave's next 64 tiles, one to a lane, for each half of a tile
     int pg[2];
     float ks[2], vlog[2];
-    uint64_t plain, odd;  // tiles: all of whose pages exist and have scales that are their logarithm, and that have another
+    uint64_t odd, plain;  // tiles with a page whose scales are not finite, or leave a rest; with no such page and none missing
     auto pages = [&](int tile) {
       const int t = tile + kWaves * lane;
 #pragma unroll
@@ -182,13 +182,14 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     };
     // once the scales are there: not before the first tile is requested
     auto logarithms = [&]() {
-      odd = 0;
+      bool some = false;
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         const ValueScale vs = value_scale(vlog[st]);
         vlog[st] = vs.log;
-        odd |= __ballot(pg[st] >= 0 && vs.rest != 1.f);
+        some |= pg[st] >= 0 && (vs.rest != 1.f || !(fabsf(ks[st]) < INFINITY));
       }
+      odd = __ballot(some);
       plain = __ballot(pg[0] >= 0 && pg[1] >= 0) & ~odd;
     };
 
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     logarithms();
     for (; tile < s1; tile += kWaves) {
       const int tok0 = blk.token(tile);
-      const float ks0 = lane_value(ks[0], i), ks1 = lane_value(ks[1], i);
+      float ks0 = lane_value(ks[0], i), ks1 = lane_value(ks[1], i);
       const float log0 = lane_value(vlog[0], i), log1 = lane_value(vlog[1], i);
       const float inv0 = inverse(log0), inv1 = inverse(log1);
       const bool is_plain = plain >> i & 1;
@@ -294,6 +295,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
       if (!is_plain) {
         pg0 = lane_value(pg[0], i), pg1 = lane_value(pg[1], i);
         if (odd >> i & 1) {  // read once more: kept, it would take registers from all tiles
+          ks0 = key_scale(ks0), ks1 = key_scale(ks1);
           if (pg0 >= 0) rest0 = value_scale(p.cache.v_scale[(int64_t)pg0 * H + h]).rest;
           if (pg1 >= 0) rest1 = value_scale(p.cache.v_scale[(int64_t)pg1 * H + h]).rest;
         }

@@ -47,6 +47,11 @@ __device__ inline float query_unit(float top) {
   return __builtin_bit_cast(float, (uint32_t)min(269 - ex, 254) << 23);
 }
 
+// An infinite key scale makes its codes' values infinite or NaN (0), and the
+// logits of a page with both NaN; infinity times the sum of codes would have a
+// sign, and a negative one would drop the token.
+__device__ inline float key_scale(float k) { return fabsf(k) < INFINITY ? k : NAN; }
+
 // A page's value scale as 2^log times rest.  rest is 1 for scales of at least
 // 2^-80; smaller ones count as 2^-80 (no logarithm for 0, and no weight that
 // leaves binary32), and it has the sign and whatever is not finite.

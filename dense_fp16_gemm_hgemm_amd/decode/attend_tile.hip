@@ -305,11 +305,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float lv = lane_value(vs.log, i);
+        const float lv = lane_value(vs.log, i), fi = key_scale(f[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const bool ok = (valid >> i & 1) && seen(16 * i + 8 * (e / 4) + e % 4);
-          const float y = ok ? __builtin_fmaf(z[i / 2][8 * (i % 2) + e], f[i], lv) : -INFINITY;
+          const float y = ok ? __builtin_fmaf(z[i / 2][8 * (i % 2) + e], fi, lv) : -INFINITY;
           z[i / 2][8 * (i % 2) + e] = y;
           top = fmaxf(top, y);
         }

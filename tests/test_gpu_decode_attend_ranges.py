@@ -141,3 +141,18 @@ def test_queries_of_very_different_channels(d, D, G, new, codes, dtype):
     q[:, :, 0] = 60000.0
     got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
     check(got, *attend(q, cache, table, lens, cu))
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("D, G, new", ROWS)
+def test_an_infinite_key_is_not_dropped(d, D, G, new, sign, codes):
+    """Alone on the last page, it makes the query that sees it not finite, whatever the query's sign."""
+    lens, page = [320 + 1], 16
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], torch.float16, 43)
+    k = torch.randn((1, 1, D), device=DEV).half()
+    k[0, 0, 3] = math.inf
+    q[:, :, 3] = sign
+    d.kv_append(cache, k, k.nan_to_num(posinf=1.0), table.to(DEV), put([320]))
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    assert not torch.isfinite(got[-1]).any() and torch.isfinite(got[:-1]).all()
