@@ -260,6 +260,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
       }
       float f = p.scale * 1.44269504088896340736f / down;
       if (CODE == MI_DECODE_INT8) f *= 1.f / kTiny;
+      if (top == INFINITY) f = NAN;  // every logit is infinite, and no softmax is left
       if constexpr (NT == 1) {
         fac[0] = f;
       } else {

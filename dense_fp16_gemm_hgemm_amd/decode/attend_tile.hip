@@ -234,6 +234,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     }
     fac = fabsf(p.scale) * 1.44269504088896340736f / down;
     if (CODE == MI_DECODE_INT8) fac *= 1.f / kTiny;
+    if (top == INFINITY) fac = NAN;  // every logit is infinite, and no softmax is left
   }
   __syncthreads();
   convert(0, 0);

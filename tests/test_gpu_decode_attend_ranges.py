@@ -156,3 +156,19 @@ def test_an_infinite_key_is_not_dropped(d, D, G, new, sign, codes):
     d.kv_append(cache, k, k.nan_to_num(posinf=1.0), table.to(DEV), put([320]))
     got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
     assert not torch.isfinite(got[-1]).any() and torch.isfinite(got[:-1]).all()
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("D, G, new", ROWS)
+def test_an_infinite_query_is_nan(d, D, G, new, value):
+    """All its logits are infinite, of either sign: no softmax is left.  Other rows keep theirs."""
+    lens, page = [100 + new], 16
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, torch.int8, torch.float16, 47)
+    cache.k[..., 5].clamp_(max=-1)  # every logit takes the sign that value has not
+    ref, bound = attend(q, cache, table, lens, cu)
+    q[0, 0, 5] = value
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    assert torch.isnan(got[0, 0]).all()
+    keep = torch.ones(q.shape[:2], dtype=torch.bool, device=DEV)
+    keep[0, 0] = False
+    check(got[keep], ref[keep], bound[keep])
