@@ -5,6 +5,7 @@
 // longer than the kernels; here they take about 5.  A call returns its result,
 // or the status of a call that the library refused; arguments that do not fit
 // raise ValueError or TypeError.  No C++ exception leaves a function.
+#include <algorithm>
 #include <cmath>
 
 #include <torch/csrc/autograd/python_variable.h>
@@ -111,6 +112,12 @@ mi_decode_batch_t batch_of(PyObject* table_o, PyObject* lens_o, PyObject* cu_o, 
   return t;
 }
 
+// The most tokens that a sequence has in the call: with cu alone, all of them.
+int32_t longest(PyObject* o, PyObject* cu, int64_t tokens, const char* name) {
+  if (o != Py_None) return number32(o, name);
+  return cu == Py_None ? 1 : (int32_t)std::min<int64_t>(tokens, INT32_MAX);
+}
+
 // A KvCache's numbers: the address of its C struct, and its device.
 const mi_decode_cache_t& cache_of(PyObject* o) { return *static_cast<const mi_decode_cache_t*>(PyLong_AsVoidPtr(o)); }
 c10::Device device_of(PyObject* o) { return c10::Device(c10::kCUDA, (c10::DeviceIndex)number(o)); }
@@ -183,7 +190,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const mi_decode_rows_t rk = rows(k, "k", c.kv_heads, c.head_dim, k), rv = rows(v, "v", c.kv_heads, c.head_dim, k);
     const int64_t T = k.size(0);
     if (v.size(0) != T) refuse(PyExc_ValueError, "k and v must have the same tokens");
-    const mi_decode_batch_t t = batch_of(a[5], a[6], a[7], T, number32(a[8], "max_new"), device, "past", "cu_new");
+    const mi_decode_batch_t t = batch_of(a[5], a[6], a[7], T, longest(a[8], a[7], T, "max_new"), device, "past", "cu_new");
     mi_decode_rows_t rq = {}, ro = {};
     at::Tensor made;
     int64_t hq = 0;
@@ -225,7 +232,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const c10::Device device = device_of(a[2]);
     const int64_t T = number(a[6]);
     if (T < 0) refuse(PyExc_ValueError, "tokens must not be negative");
-    const mi_decode_batch_t t = batch_of(a[3], a[4], a[5], T, number32(a[7], "max_tokens"), device, "start", "cu");
+    const mi_decode_batch_t t = batch_of(a[3], a[4], a[5], T, longest(a[7], a[5], T, "max_tokens"), device, "start", "cu");
     const bool bf16 = PyObject_IsTrue(a[8]);
     const auto options = at::TensorOptions().dtype(bf16 ? at::kBFloat16 : at::kHalf).device(device);
     const at::Tensor k = at::empty({T, c.kv_heads, c.head_dim}, options), v = at::empty({T, c.kv_heads, c.head_dim}, options);
@@ -252,7 +259,7 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (hq < 1 || hq % c.kv_heads) refuse(PyExc_ValueError, "q must have a multiple of %d heads, got %lld", c.kv_heads, (long long)hq);
     const int32_t window = number32(a[9], "window"), sinks = number32(a[10], "sinks");
     if (window < 0 || sinks < 0) refuse(PyExc_ValueError, "window and sinks must not be negative");
-    const mi_decode_batch_t t = batch_of(a[4], a[5], a[6], T, number32(a[7], "max_q"), device, "lens", "cu_q");
+    const mi_decode_batch_t t = batch_of(a[4], a[5], a[6], T, longest(a[7], a[6], T, "max_q"), device, "lens", "cu_q");
     const int64_t max_len = a[8] == Py_None ? (int64_t)t.table_cols * c.page_size : number(a[8]);
     const double scale = a[11] == Py_None ? 1.0 / std::sqrt((double)c.head_dim) : PyFloat_AsDouble(a[11]);
     if (PyErr_Occurred()) throw Refused{};

@@ -293,10 +293,12 @@ class Decode:
         return _done(_calls.w4_linear(self.handle, x, qweight, scales, zeros, n, group, bias, out, _raw(stream)),
                      "mi_decode_w4_linear")
 
-    def kv_append(self, cache, k, v, table, past, cu_new=None, max_new=1, *, q=None, rope=None,
+    def kv_append(self, cache, k, v, table, past, cu_new=None, max_new=None, *, q=None, rope=None,
                   interleaved=False, q_out=None, stream=None):
         """Append k and v [tokens, kv_heads, head_dim] after the `past` tokens of each sequence;
-        returns q [tokens, q_heads, head_dim] turned by its positions (None without q)."""
+        returns q [tokens, q_heads, head_dim] turned by its positions (None without q).
+        Without cu_new one token a sequence; max_new: the most that a sequence has of them,
+        which saves work where it is far below all tokens (the default with cu_new)."""
         return _done(_calls.kv_append(self.handle, cache._at, cache._dev, k, v, table, past, cu_new, max_new, q, rope,
                                       interleaved, q_out, _raw(stream)), "mi_decode_kv_append")
 
@@ -307,13 +309,14 @@ class Decode:
         if dtype not in _DTYPES:
             raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
         T = start.shape[0] if tokens is None else tokens
-        most = (1 if cu is None else T) if max_tokens is None else max_tokens
-        return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, T, most,
+        return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, T, max_tokens,
                                     dtype == torch.bfloat16, _raw(stream)), "mi_decode_kv_read")
 
-    def kv_attend(self, q, cache, table, lens, cu_q=None, max_q=1, *, max_len=None, window=0, sinks=0,
+    def kv_attend(self, q, cache, table, lens, cu_q=None, max_q=None, *, max_len=None, window=0, sinks=0,
                   scale=None, out=None, stream=None):
         """softmax(scale q k^T) v over the cache for q [tokens, q_heads, head_dim]: each
-        sequence's queries are the last of its lens[b] tokens.  scale: head_dim ** -0.5."""
+        sequence's queries are the last of its lens[b] tokens.  Without cu_q one query a
+        sequence; max_q: the most that a sequence has, which saves work where it is far
+        below all queries (the default with cu_q).  scale: head_dim ** -0.5."""
         return _done(_calls.kv_attend(self.handle, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
                                       window, sinks, scale, out, _raw(stream)), "mi_decode_kv_attend")

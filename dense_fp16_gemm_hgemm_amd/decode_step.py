@@ -89,9 +89,9 @@ class Model:
             return self.decode.w4_linear(x, w.w4.qweight, w.w4.scales, w.w4.zeros, n=w.w4.n, group=w.w4.group)
         return self.gemm.run(x, w.full)
 
-    def forward(self, x, cu=None, most=1, max_len=None):
-        """x [tokens, hidden]: the next tokens of every sequence, one each, or as `cu` says; they
-        join the cache, and the layers' output for them is returned."""
+    def forward(self, x, cu=None, most=None, max_len=None):
+        """x [tokens, hidden]: the next tokens of every sequence, one each, or as `cu` says (`most`
+        at most, if given); they join the cache, and the layers' output for them is returned."""
         c, d = self.config, self.decode
         few = cu is None
         new = 1 if few else cu[1:] - cu[:-1]

@@ -1,0 +1,35 @@
+"""Calls of the decode operators that leave arguments out, or name another stream."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+decode = pytest.importorskip("dense_fp16_gemm_hgemm_amd.decode")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+from test_gpu_decode_attend import check, make, put  # noqa: E402
+
+DEV = torch.device("cuda", 0)
+
+
+@pytest.fixture(scope="module")
+def d():
+    h = decode.Decode()
+    yield h
+    h.close()
+
+
+@pytest.mark.parametrize("new", [[40, 1, 0, 100], [3, 5, 2, 1]])
+def test_ragged_calls_without_a_longest_sequence(d, new):
+    """cu alone says how many tokens there are: all of them are appended and all rows are computed."""
+    past = [10, 0, 33, 64]
+    lens = [p + n for p, n in zip(past, new)]
+    cache, table, cu, q = make(lens, new, 8, 2, 64, 16, torch.int8, torch.float16, 61)
+    other = decode.KvCache(*[x.clone() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)])
+    k, v = (torch.randn((cu[-1], 2, 64), device=DEV).half() for _ in range(2))
+    dt = table.to(DEV)
+    d.kv_append(cache, k, v, dt, put(past), put(cu))
+    d.kv_append(other, k, v, dt, put(past), put(cu), max(new))
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x, y = getattr(cache, name), getattr(other, name)
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
+    check(d.kv_attend(q, cache, dt, put(lens), put(cu)), cache, q, table, lens, cu)
