@@ -305,11 +305,15 @@ class Decode:
     def kv_read(self, cache, table, start, cu=None, *, tokens=None, max_tokens=None, dtype=torch.float16,
                 stream=None):
         """The values of the cached tokens at positions start[b] + i, i < cu[b + 1] - cu[b]:
-        k and v [tokens, kv_heads, head_dim].  Without cu one token a sequence."""
+        k and v [tokens, kv_heads, head_dim].  Without cu one token a sequence; with it
+        `tokens` is needed, how many there are in all (cu lies on the device)."""
         if dtype not in _DTYPES:
             raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
-        T = start.shape[0] if tokens is None else tokens
-        return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, T, max_tokens,
+        if tokens is None:
+            if cu is not None:
+                raise ValueError("kv_read needs tokens, the number of tokens in all, where cu is given")
+            tokens = start.shape[0]
+        return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, tokens, max_tokens,
                                     dtype == torch.bfloat16, _raw(stream)), "mi_decode_kv_read")
 
     def kv_attend(self, q, cache, table, lens, cu_q=None, max_q=None, *, max_len=None, window=0, sinks=0,

@@ -33,3 +33,14 @@ def test_ragged_calls_without_a_longest_sequence(d, new):
         x, y = getattr(cache, name), getattr(other, name)
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
     check(d.kv_attend(q, cache, dt, put(lens), put(cu)), cache, q, table, lens, cu)
+
+
+def test_kv_read_needs_the_number_of_tokens(d):
+    """cu lies on the device: without `tokens` only as many as there are sequences were read."""
+    cache = decode.KvCache.empty(8, 2, 64, 16)
+    table, start, cu = put([[0, 1], [2, 3]]), put([0, 0]), put([0, 20, 25])
+    with pytest.raises(ValueError, match="tokens"):
+        d.kv_read(cache, table, start, cu)
+    k, v = d.kv_read(cache, table, start, cu, tokens=25)
+    assert k.shape == v.shape == (25, 2, 64)
+    assert d.kv_read(cache, table, start)[0].shape == (2, 2, 64)
