@@ -9,7 +9,9 @@
 #include <cmath>
 
 #include <torch/csrc/autograd/python_variable.h>
+#include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 
 #include "mi_decode.h"
@@ -58,10 +60,24 @@ void on(const at::Tensor* x, c10::Device device, const char* name) {
   if (x && x->device() != device)
     refuse(PyExc_ValueError, "%s must be on %s, got %s", name, device.str().c_str(), x->device().str().c_str());
 }
-void* stream_of(PyObject* o, c10::Device device) {
-  if (o != Py_None) return PyLong_AsVoidPtr(o);
-  return c10::hip::getCurrentHIPStream(device.index()).stream();
-}
+// The stream of a call: the current one, or one that the caller names, which is
+// the current one then while the call makes its results.  Their memory belongs
+// to it: memory of another stream could still be in use there, or be given out
+// there again before the kernel has written it.
+struct OnStream {
+  void* raw;
+  c10::OptionalStreamGuard guard;
+  OnStream(PyObject* o, c10::Device device) {
+    if (o == Py_None) {
+      raw = c10::hip::getCurrentHIPStream(device.index()).stream();
+      return;
+    }
+    raw = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Refused{};
+    guard.reset_stream(
+        c10::hip::getStreamFromExternalMasqueradingAsCUDA(static_cast<hipStream_t>(raw), device.index()).unwrap());
+  }
+};
 
 bool is(const at::Tensor& x, at::ScalarType t, std::initializer_list<int64_t> shape) {
   return x.scalar_type() == t && x.sizes() == c10::IntArrayRef(shape) && x.is_contiguous();
@@ -149,6 +165,7 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1)) refuse(PyExc_ValueError, "x must be 2-D with unit-stride rows");
     const mi_decode_dtype_t type = type16(x, "x");
     if (!x.is_cuda()) refuse(PyExc_ValueError, "x must be on the GPU");
+    const OnStream stream(a[9], x.device());
     if (n < 0) refuse(PyExc_ValueError, "n must not be negative");
     if (group < 32 || group % 32) refuse(PyExc_ValueError, "group must be a positive multiple of 32, got %lld", (long long)group);
     const int64_t M = x.size(0), K = x.size(1), nb = (n + 15) / 16, kb = (K + 127) / 128, groups = (K + group - 1) / group;
@@ -175,7 +192,7 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(out, x.device(), "out");
     return result(mi_decode_w4_linear(handle(a[0]), type, M, n, K, group, x.data_ptr(), x.stride(0), qw.data_ptr(),
                                       sc.data_ptr(), zeros ? zeros->data_ptr() : nullptr, bias ? bias->data_ptr() : nullptr,
-                                      out->data_ptr(), out->stride(0), stream_of(a[9], x.device())), *out);
+                                      out->data_ptr(), out->stride(0), stream.raw), *out);
   });
 }
 
@@ -184,6 +201,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return call(n_args, 14, [&]() -> PyObject* {
     const mi_decode_cache_t& c = cache_of(a[1]);
     const c10::Device device = device_of(a[2]);
+    const OnStream stream(a[13], device);
     const at::Tensor &k = *tensor(a[3], "k"), &v = *tensor(a[4], "v");
     const at::Tensor *q = maybe(a[9], "q"), *rope = maybe(a[10], "rope"), *q_out = maybe(a[12], "q_out");
     const mi_decode_dtype_t type = type16(k, "k");
@@ -219,7 +237,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const mi_decode_status_t st = mi_decode_kv_append(
         handle(a[0]), &c, type, &t, &rk, &rv, rope ? static_cast<const float*>(rope->data_ptr()) : nullptr,
         rope ? rope->size(0) : 0, rope ? (int32_t)rope->size(1) : 0, on_pairs, (int32_t)hq, q ? &rq : nullptr,
-        q ? &ro : nullptr, stream_of(a[13], device));
+        q ? &ro : nullptr, stream.raw);
     if (st != MI_DECODE_OK || q) return result(st, q ? *q_out : k);
     Py_RETURN_NONE;
   });
@@ -230,6 +248,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return call(n_args, 10, [&]() -> PyObject* {
     const mi_decode_cache_t& c = cache_of(a[1]);
     const c10::Device device = device_of(a[2]);
+    const OnStream stream(a[9], device);
     const int64_t T = number(a[6]);
     if (T < 0) refuse(PyExc_ValueError, "tokens must not be negative");
     const mi_decode_batch_t t = batch_of(a[3], a[4], a[5], T, longest(a[7], a[5], T, "max_tokens"), device, "start", "cu");
@@ -237,7 +256,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto options = at::TensorOptions().dtype(bf16 ? at::kBFloat16 : at::kHalf).device(device);
     const at::Tensor k = at::empty({T, c.kv_heads, c.head_dim}, options), v = at::empty({T, c.kv_heads, c.head_dim}, options);
     const mi_decode_status_t st = mi_decode_kv_read(handle(a[0]), &c, bf16 ? MI_DECODE_BF16 : MI_DECODE_F16, &t, k.data_ptr(),
-                                                    v.data_ptr(), stream_of(a[9], device));
+                                                    v.data_ptr(), stream.raw);
     if (st != MI_DECODE_OK) return PyLong_FromLong(st);
     PyObject *pk = THPVariable_Wrap(k), *pv = THPVariable_Wrap(v), *both = pk && pv ? PyTuple_Pack(2, pk, pv) : nullptr;
     Py_XDECREF(pk);
@@ -251,6 +270,7 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return call(n_args, 14, [&]() -> PyObject* {
     const mi_decode_cache_t& c = cache_of(a[1]);
     const c10::Device device = device_of(a[2]);
+    const OnStream stream(a[13], device);
     const at::Tensor& q = *tensor(a[3], "q");
     const mi_decode_dtype_t type = type16(q, "q");
     const int64_t hq = q.dim() == 3 ? q.size(1) : -1;
@@ -275,7 +295,7 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(&q, device, "q");
     on(out, device, "out");
     return result(mi_decode_kv_attend(handle(a[0]), &c, type, &t, max_len, (int32_t)hq, &rq, &ro, (float)scale, window, sinks,
-                                      stream_of(a[13], device)), *out);
+                                      stream.raw), *out);
   });
 }
 

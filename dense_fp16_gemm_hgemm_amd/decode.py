@@ -11,7 +11,9 @@ Operations, layouts and rules are those of ``include/mi_decode.h``; torch suppli
 memory and the stream.  The four calls check and marshal their arguments in an extension
 module (``bind/decode_calls.cpp``), because a decode step's kernels take microseconds; the
 rest of the library is reached with ctypes.  A call returns
-without synchronising, and every call may be captured into a graph.  ``kv_attend`` uses the
+without synchronising, and every call may be captured into a graph.  Work goes to the
+current stream, or to ``stream`` (a torch stream, or a handle as an integer), whose memory
+the results are then, as if it were the current one.  ``kv_attend`` uses the
 handle's workspace: calls that may overlap on different streams need handles of their own.
 
     from dense_fp16_gemm_hgemm_amd import decode
@@ -120,8 +122,13 @@ def _on(device, **tensors):
             raise ValueError(f"{name} must be on {device}, got {x.device}")
 
 
-def _raw(stream):
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+def _raw(stream, device):
+    """A stream's handle: of a torch stream on `device`, or an integer as it is."""
+    if not isinstance(stream, torch.cuda.Stream):
+        return stream
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
+    return stream.cuda_stream
 
 
 def _done(result, what):
@@ -290,7 +297,8 @@ class Decode:
 
     def w4_linear(self, x, qweight, scales, zeros=None, *, n, group=128, bias=None, out=None, stream=None):
         """x [M, K] times the 4-bit weights [n, K]: [M, n] in x's type, sums in float32."""
-        return _done(_calls.w4_linear(self.handle, x, qweight, scales, zeros, n, group, bias, out, _raw(stream)),
+        return _done(_calls.w4_linear(self.handle, x, qweight, scales, zeros, n, group, bias, out,
+                                      stream if stream is None else _raw(stream, x.device)),
                      "mi_decode_w4_linear")
 
     def kv_append(self, cache, k, v, table, past, cu_new=None, max_new=None, *, q=None, rope=None,
@@ -300,7 +308,7 @@ class Decode:
         Without cu_new one token a sequence; max_new: the most that a sequence has of them,
         which saves work where it is far below all tokens (the default with cu_new)."""
         return _done(_calls.kv_append(self.handle, cache._at, cache._dev, k, v, table, past, cu_new, max_new, q, rope,
-                                      interleaved, q_out, _raw(stream)), "mi_decode_kv_append")
+                                      interleaved, q_out, stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_append")
 
     def kv_read(self, cache, table, start, cu=None, *, tokens=None, max_tokens=None, dtype=torch.float16,
                 stream=None):
@@ -314,7 +322,8 @@ class Decode:
                 raise ValueError("kv_read needs tokens, the number of tokens in all, where cu is given")
             tokens = start.shape[0]
         return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, tokens, max_tokens,
-                                    dtype == torch.bfloat16, _raw(stream)), "mi_decode_kv_read")
+                                    dtype == torch.bfloat16,
+                                    stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_read")
 
     def kv_attend(self, q, cache, table, lens, cu_q=None, max_q=None, *, max_len=None, window=0, sinks=0,
                   scale=None, out=None, stream=None):
@@ -323,4 +332,5 @@ class Decode:
         sequence; max_q: the most that a sequence has, which saves work where it is far
         below all queries (the default with cu_q).  scale: head_dim ** -0.5."""
         return _done(_calls.kv_attend(self.handle, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
-                                      window, sinks, scale, out, _raw(stream)), "mi_decode_kv_attend")
+                                      window, sinks, scale, out,
+                                      stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_attend")

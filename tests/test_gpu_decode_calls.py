@@ -44,3 +44,43 @@ def test_kv_read_needs_the_number_of_tokens(d):
     k, v = d.kv_read(cache, table, start, cu, tokens=25)
     assert k.shape == v.shape == (25, 2, 64)
     assert d.kv_read(cache, table, start)[0].shape == (2, 2, 64)
+
+
+def owner(x):
+    """The stream that the allocator keeps a tensor's memory for."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= x.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_results_belong_to_the_stream_that_is_named(d):
+    """Each call with stream= and no out: its memory, and its values beside work on both streams."""
+    lens = [300, 41]
+    cache, table, cu, q = make(lens, [1, 1], 8, 2, 64, 16, torch.int8, torch.float16, 67)
+    w = decode.w4_quantize(torch.randn((256, 512), device=DEV).half())
+    x, kv = torch.randn((4, 512), device=DEV).half(), torch.randn((2, 2, 64), device=DEV).half()
+    table, rope = table.to(DEV), decode.rope_table(table.shape[1] * 16, 64)
+    dl, past = put(lens), put([n - 1 for n in lens])
+
+    def calls(**kw):
+        yield "w4_linear", d.w4_linear(x, w.qweight, w.scales, n=256, **kw)
+        yield "kv_append", d.kv_append(cache, kv, kv, table, past, q=q, rope=rope, **kw)
+        yield "kv_read k", d.kv_read(cache, table, past, **kw)[0]
+        yield "kv_read v", d.kv_read(cache, table, past, **kw)[1]
+        yield "kv_attend", d.kv_attend(q, cache, table, dl, **kw)
+
+    want = dict(calls())
+    busy = torch.randn((2048, 2048), device=DEV)
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            busy @ busy
+        for name, got in calls(stream=handle):
+            assert owner(got) == side.cuda_stream, name
+            torch.full_like(got, 7.0)  # on the current stream: not the same memory
+            side.synchronize()
+            assert torch.equal(got, want[name]), name
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    with pytest.raises(TypeError):
+        d.w4_linear(x, w.qweight, w.scales, n=256, stream="side")
