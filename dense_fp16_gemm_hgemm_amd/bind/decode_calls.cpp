@@ -60,6 +60,12 @@ void on(const at::Tensor* x, c10::Device device, const char* name) {
   if (x && x->device() != device)
     refuse(PyExc_ValueError, "%s must be on %s, got %s", name, device.str().c_str(), x->device().str().c_str());
 }
+// Kernels run on the handle's device, and with its workspace; -1: an inspection handle.
+void same_device(PyObject* handle_device, c10::Device device) {
+  const int64_t d = number(handle_device);
+  if (d >= 0 && d != device.index())
+    refuse(PyExc_ValueError, "the handle is on cuda:%d, the tensors on cuda:%d", (int)d, (int)device.index());
+}
 // The stream of a call: the current one, or one that the caller names, which is
 // the current one then while the call makes its results.  Their memory belongs
 // to it: memory of another stream could still be in use there, or be given out
@@ -156,16 +162,17 @@ PyObject* call(Py_ssize_t got, Py_ssize_t want, F f) {
   return nullptr;
 }
 
-// handle, x, qweight, scales, zeros, n, group, bias, out, stream
+// handle, its device, x, qweight, scales, zeros, n, group, bias, out, stream
 PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call(n_args, 10, [&]() -> PyObject* {
-    const at::Tensor &x = *tensor(a[1], "x"), &qw = *tensor(a[2], "qweight"), &sc = *tensor(a[3], "scales");
-    const at::Tensor *zeros = maybe(a[4], "zeros"), *bias = maybe(a[7], "bias");
-    const int64_t n = number(a[5]), group = number(a[6]);
+  return call(n_args, 11, [&]() -> PyObject* {
+    const at::Tensor &x = *tensor(a[2], "x"), &qw = *tensor(a[3], "qweight"), &sc = *tensor(a[4], "scales");
+    const at::Tensor *zeros = maybe(a[5], "zeros"), *bias = maybe(a[8], "bias");
+    const int64_t n = number(a[6]), group = number(a[7]);
     if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1)) refuse(PyExc_ValueError, "x must be 2-D with unit-stride rows");
     const mi_decode_dtype_t type = type16(x, "x");
     if (!x.is_cuda()) refuse(PyExc_ValueError, "x must be on the GPU");
-    const OnStream stream(a[9], x.device());
+    same_device(a[1], x.device());
+    const OnStream stream(a[10], x.device());
     if (n < 0) refuse(PyExc_ValueError, "n must not be negative");
     if (group < 32 || group % 32) refuse(PyExc_ValueError, "group must be a positive multiple of 32, got %lld", (long long)group);
     const int64_t M = x.size(0), K = x.size(1), nb = (n + 15) / 16, kb = (K + 127) / 128, groups = (K + group - 1) / group;
@@ -178,7 +185,7 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (bias && (bias->scalar_type() != x.scalar_type() || bias->dim() != 1 || bias->size(0) != n || (n > 1 && bias->stride(0) != 1)))
       refuse(PyExc_ValueError, "bias must be contiguous, of x's type and (%lld,)", (long long)n);
     at::Tensor made;
-    const at::Tensor* out = maybe(a[8], "out");
+    const at::Tensor* out = maybe(a[9], "out");
     if (!out) {
       made = at::empty({M, n}, x.options());
       out = &made;
@@ -196,19 +203,20 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// handle, cache, device, k, v, table, past, cu_new, max_new, q, rope, interleaved, q_out, stream
+// handle, its device, cache, device, k, v, table, past, cu_new, max_new, q, rope, interleaved, q_out, stream
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call(n_args, 14, [&]() -> PyObject* {
-    const mi_decode_cache_t& c = cache_of(a[1]);
-    const c10::Device device = device_of(a[2]);
-    const OnStream stream(a[13], device);
-    const at::Tensor &k = *tensor(a[3], "k"), &v = *tensor(a[4], "v");
-    const at::Tensor *q = maybe(a[9], "q"), *rope = maybe(a[10], "rope"), *q_out = maybe(a[12], "q_out");
+  return call(n_args, 15, [&]() -> PyObject* {
+    const mi_decode_cache_t& c = cache_of(a[2]);
+    const c10::Device device = device_of(a[3]);
+    same_device(a[1], device);
+    const OnStream stream(a[14], device);
+    const at::Tensor &k = *tensor(a[4], "k"), &v = *tensor(a[5], "v");
+    const at::Tensor *q = maybe(a[10], "q"), *rope = maybe(a[11], "rope"), *q_out = maybe(a[13], "q_out");
     const mi_decode_dtype_t type = type16(k, "k");
     const mi_decode_rows_t rk = rows(k, "k", c.kv_heads, c.head_dim, k), rv = rows(v, "v", c.kv_heads, c.head_dim, k);
     const int64_t T = k.size(0);
     if (v.size(0) != T) refuse(PyExc_ValueError, "k and v must have the same tokens");
-    const mi_decode_batch_t t = batch_of(a[5], a[6], a[7], T, longest(a[8], a[7], T, "max_new"), device, "past", "cu_new");
+    const mi_decode_batch_t t = batch_of(a[6], a[7], a[8], T, longest(a[9], a[8], T, "max_new"), device, "past", "cu_new");
     mi_decode_rows_t rq = {}, ro = {};
     at::Tensor made;
     int64_t hq = 0;
@@ -232,7 +240,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(q, device, "q");
     if (q) on(q_out, device, "q_out");
     on(rope, device, "rope");
-    const int on_pairs = PyObject_IsTrue(a[11]);
+    const int on_pairs = PyObject_IsTrue(a[12]);
     if (on_pairs < 0) throw Refused{};
     const mi_decode_status_t st = mi_decode_kv_append(
         handle(a[0]), &c, type, &t, &rk, &rv, rope ? static_cast<const float*>(rope->data_ptr()) : nullptr,
@@ -243,16 +251,17 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// handle, cache, device, table, start, cu, tokens, max_tokens, bf16, stream
+// handle, its device, cache, device, table, start, cu, tokens, max_tokens, bf16, stream
 PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call(n_args, 10, [&]() -> PyObject* {
-    const mi_decode_cache_t& c = cache_of(a[1]);
-    const c10::Device device = device_of(a[2]);
-    const OnStream stream(a[9], device);
-    const int64_t T = number(a[6]);
+  return call(n_args, 11, [&]() -> PyObject* {
+    const mi_decode_cache_t& c = cache_of(a[2]);
+    const c10::Device device = device_of(a[3]);
+    same_device(a[1], device);
+    const OnStream stream(a[10], device);
+    const int64_t T = number(a[7]);
     if (T < 0) refuse(PyExc_ValueError, "tokens must not be negative");
-    const mi_decode_batch_t t = batch_of(a[3], a[4], a[5], T, longest(a[7], a[5], T, "max_tokens"), device, "start", "cu");
-    const bool bf16 = PyObject_IsTrue(a[8]);
+    const mi_decode_batch_t t = batch_of(a[4], a[5], a[6], T, longest(a[8], a[6], T, "max_tokens"), device, "start", "cu");
+    const bool bf16 = PyObject_IsTrue(a[9]);
     const auto options = at::TensorOptions().dtype(bf16 ? at::kBFloat16 : at::kHalf).device(device);
     const at::Tensor k = at::empty({T, c.kv_heads, c.head_dim}, options), v = at::empty({T, c.kv_heads, c.head_dim}, options);
     const mi_decode_status_t st = mi_decode_kv_read(handle(a[0]), &c, bf16 ? MI_DECODE_BF16 : MI_DECODE_F16, &t, k.data_ptr(),
@@ -265,26 +274,27 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// handle, cache, device, q, table, lens, cu_q, max_q, max_len, window, sinks, scale, out, stream
+// handle, its device, cache, device, q, table, lens, cu_q, max_q, max_len, window, sinks, scale, out, stream
 PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call(n_args, 14, [&]() -> PyObject* {
-    const mi_decode_cache_t& c = cache_of(a[1]);
-    const c10::Device device = device_of(a[2]);
-    const OnStream stream(a[13], device);
-    const at::Tensor& q = *tensor(a[3], "q");
+  return call(n_args, 15, [&]() -> PyObject* {
+    const mi_decode_cache_t& c = cache_of(a[2]);
+    const c10::Device device = device_of(a[3]);
+    same_device(a[1], device);
+    const OnStream stream(a[14], device);
+    const at::Tensor& q = *tensor(a[4], "q");
     const mi_decode_dtype_t type = type16(q, "q");
     const int64_t hq = q.dim() == 3 ? q.size(1) : -1;
     const mi_decode_rows_t rq = rows(q, "q", hq, c.head_dim, q);
     const int64_t T = q.size(0);
     if (hq < 1 || hq % c.kv_heads) refuse(PyExc_ValueError, "q must have a multiple of %d heads, got %lld", c.kv_heads, (long long)hq);
-    const int32_t window = number32(a[9], "window"), sinks = number32(a[10], "sinks");
+    const int32_t window = number32(a[10], "window"), sinks = number32(a[11], "sinks");
     if (window < 0 || sinks < 0) refuse(PyExc_ValueError, "window and sinks must not be negative");
-    const mi_decode_batch_t t = batch_of(a[4], a[5], a[6], T, longest(a[7], a[6], T, "max_q"), device, "lens", "cu_q");
-    const int64_t max_len = a[8] == Py_None ? (int64_t)t.table_cols * c.page_size : number(a[8]);
-    const double scale = a[11] == Py_None ? 1.0 / std::sqrt((double)c.head_dim) : PyFloat_AsDouble(a[11]);
+    const mi_decode_batch_t t = batch_of(a[5], a[6], a[7], T, longest(a[8], a[7], T, "max_q"), device, "lens", "cu_q");
+    const int64_t max_len = a[9] == Py_None ? (int64_t)t.table_cols * c.page_size : number(a[9]);
+    const double scale = a[12] == Py_None ? 1.0 / std::sqrt((double)c.head_dim) : PyFloat_AsDouble(a[12]);
     if (PyErr_Occurred()) throw Refused{};
     at::Tensor made;
-    const at::Tensor* out = maybe(a[12], "out");
+    const at::Tensor* out = maybe(a[13], "out");
     if (!out) {
       made = at::empty({T, hq, c.head_dim}, q.options());
       out = &made;

@@ -81,6 +81,7 @@ def _sig(name, restype, *argtypes):
 
 _create = _sig("mi_decode_create", ctypes.c_int, ctypes.POINTER(_p), _u32)
 _destroy = _sig("mi_decode_destroy", ctypes.c_int, _p)
+_device = _sig("mi_decode_device", ctypes.c_int, _p)
 _status_string = _sig("mi_decode_status_string", ctypes.c_char_p, ctypes.c_int)
 _last_hip_error = _sig("mi_decode_last_hip_error", ctypes.c_int, _p)
 _w4_linear = _sig("mi_decode_w4_linear", ctypes.c_int, _p, ctypes.c_int, _i64, _i64, _i64, _i64, _p,
@@ -268,12 +269,13 @@ class KvCache:
 # -------------------------------------------------------------- handle --
 
 class Decode:
-    """A library handle on the current device."""
+    """A library handle on the current device; its calls take tensors of that device."""
 
     def __init__(self, inspect_only: bool = False):
         h = _p()
         _check(_create(_byref(h), MI_DECODE_CREATE_NO_DEVICE if inspect_only else 0), "mi_decode_create")
         self.handle = h.value
+        self.device = _device(h)  # -1: inspect_only
 
     def close(self):
         if getattr(self, "handle", None):
@@ -297,7 +299,7 @@ class Decode:
 
     def w4_linear(self, x, qweight, scales, zeros=None, *, n, group=128, bias=None, out=None, stream=None):
         """x [M, K] times the 4-bit weights [n, K]: [M, n] in x's type, sums in float32."""
-        return _done(_calls.w4_linear(self.handle, x, qweight, scales, zeros, n, group, bias, out,
+        return _done(_calls.w4_linear(self.handle, self.device, x, qweight, scales, zeros, n, group, bias, out,
                                       stream if stream is None else _raw(stream, x.device)),
                      "mi_decode_w4_linear")
 
@@ -307,7 +309,7 @@ class Decode:
         returns q [tokens, q_heads, head_dim] turned by its positions (None without q).
         Without cu_new one token a sequence; max_new: the most that a sequence has of them,
         which saves work where it is far below all tokens (the default with cu_new)."""
-        return _done(_calls.kv_append(self.handle, cache._at, cache._dev, k, v, table, past, cu_new, max_new, q, rope,
+        return _done(_calls.kv_append(self.handle, self.device, cache._at, cache._dev, k, v, table, past, cu_new, max_new, q, rope,
                                       interleaved, q_out, stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_append")
 
     def kv_read(self, cache, table, start, cu=None, *, tokens=None, max_tokens=None, dtype=torch.float16,
@@ -321,7 +323,7 @@ class Decode:
             if cu is not None:
                 raise ValueError("kv_read needs tokens, the number of tokens in all, where cu is given")
             tokens = start.shape[0]
-        return _done(_calls.kv_read(self.handle, cache._at, cache._dev, table, start, cu, tokens, max_tokens,
+        return _done(_calls.kv_read(self.handle, self.device, cache._at, cache._dev, table, start, cu, tokens, max_tokens,
                                     dtype == torch.bfloat16,
                                     stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_read")
 
@@ -331,6 +333,6 @@ class Decode:
         sequence's queries are the last of its lens[b] tokens.  Without cu_q one query a
         sequence; max_q: the most that a sequence has, which saves work where it is far
         below all queries (the default with cu_q).  scale: head_dim ** -0.5."""
-        return _done(_calls.kv_attend(self.handle, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
+        return _done(_calls.kv_attend(self.handle, self.device, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
                                       window, sinks, scale, out,
                                       stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_attend")

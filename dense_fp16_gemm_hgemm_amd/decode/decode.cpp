@@ -148,6 +148,8 @@ mi_decode_status_t mi_decode_destroy(mi_decode_handle_t h) {
   return MI_DECODE_OK;
 }
 
+int mi_decode_device(mi_decode_handle_t h) { return h ? h->device : -1; }
+
 const char* mi_decode_status_string(mi_decode_status_t s) {
   switch (s) {
     case MI_DECODE_OK: return "MI_DECODE_OK";

@@ -63,6 +63,9 @@ mi_decode_status_t mi_decode_create(mi_decode_handle_t* out, uint32_t flags);
 /* Release a handle (NULL is a no-op).  Waits for nothing. */
 mi_decode_status_t mi_decode_destroy(mi_decode_handle_t h);
 
+/* The HIP device of a handle, or -1 (NULL, or an inspection handle). */
+int mi_decode_device(mi_decode_handle_t h);
+
 /* Human-readable name of a status.  Never NULL. */
 const char* mi_decode_status_string(mi_decode_status_t s);
 

@@ -84,3 +84,19 @@ def test_results_belong_to_the_stream_that_is_named(d):
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
     with pytest.raises(TypeError):
         d.w4_linear(x, w.qweight, w.scales, n=256, stream="side")
+
+
+def test_a_handle_of_another_device_is_refused(d):
+    """Its kernels would run there, with a workspace of that device."""
+    cache, table, cu, q = make([20], [1], 8, 2, 64, 16, torch.int8, torch.float16, 71)
+    w = decode.w4_quantize(torch.randn((32, 64), device=DEV).half(), 64)
+    x, kv, table = torch.zeros((1, 64), device=DEV).half(), torch.zeros((1, 2, 64), device=DEV).half(), table.to(DEV)
+    with decode.Decode() as other:
+        assert other.device == torch.cuda.current_device() == d.device
+        other.device += 1  # as a handle that was made there
+        for call in (lambda: other.w4_linear(x, w.qweight, w.scales, n=32, group=64),
+                     lambda: other.kv_append(cache, kv, kv, table, put([3])),
+                     lambda: other.kv_read(cache, table, put([3])),
+                     lambda: other.kv_attend(q, cache, table, put([20]))):
+            with pytest.raises(ValueError, match="handle is on cuda"):
+                call()
