@@ -230,7 +230,8 @@ def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda
 class KvCache:
     """A paged cache: k and v [pages, kv_heads, page_size, head_dim] of int8 or float8_e4m3fn
     codes, k_scale and v_scale float32 [pages, kv_heads].  A value is its code times its
-    page's and head's scale."""
+    page's and head's scale.  Calls go by the tensors' addresses, so a cache keeps the tensors
+    that it was made of: their elements may change, the attributes may not."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim",
                  "device", "_struct", "_at", "_dev")
@@ -256,6 +257,11 @@ class KvCache:
         self._struct = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                               self.pages, self.kv_heads, self.page_size, self.head_dim, _CODES[k.dtype])
         self._at, self._dev = ctypes.addressof(self._struct), k.device.index
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_dev"):
+            raise AttributeError(f"a KvCache keeps the tensors that it was made of: {name} cannot be set")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def empty(cls, pages, kv_heads, head_dim, page_size=64, dtype=torch.int8, device="cuda"):

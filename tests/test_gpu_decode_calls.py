@@ -100,3 +100,14 @@ def test_a_handle_of_another_device_is_refused(d):
                      lambda: other.kv_attend(q, cache, table, put([20]))):
             with pytest.raises(ValueError, match="handle is on cuda"):
                 call()
+
+
+def test_a_cache_keeps_its_tensors(d):
+    """Another tensor in its place would be shown by the attribute, and not be what the kernels use."""
+    cache = decode.KvCache.empty(4, 2, 64, 16)
+    for name in ("k", "v", "k_scale", "v_scale", "pages", "page_size", "device"):
+        value = getattr(cache, name)
+        with pytest.raises(AttributeError):
+            setattr(cache, name, value)
+    cache.k_scale.fill_(2.0)  # elements may change
+    assert float(cache.k_scale[0, 0]) == 2.0
