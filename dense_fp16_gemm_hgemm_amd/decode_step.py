@@ -112,11 +112,15 @@ class Model:
         """forward for one token a sequence as a graph: (graph, its input, its output).  The
         graph reads lengths and pages when it is replayed, and advances the lengths."""
         keep, at, out = self.lens.clone(), x.clone(), None
+        # the warm-up has no pages: x may be anything, and in the caches a large number would
+        # grow the scales of pages that hold tokens already
+        table, self.table = self.table, torch.full_like(self.table, -1)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            self.forward(at)  # warm-up; its token's slot is written again by the first replay
+            self.forward(at)
         torch.cuda.current_stream().wait_stream(side)
+        self.table = table
         self.lens.copy_(keep)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):

@@ -6,6 +6,7 @@ pytestmark = pytest.mark.gpu
 decode = pytest.importorskip("dense_fp16_gemm_hgemm_amd.decode")
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
+from dense_fp16_gemm_hgemm_amd import decode_step  # noqa: E402
 from test_gpu_decode_attend import check, make, put  # noqa: E402
 
 DEV = torch.device("cuda", 0)
@@ -111,3 +112,22 @@ def test_a_cache_keeps_its_tensors(d):
             setattr(cache, name, value)
     cache.k_scale.fill_(2.0)  # elements may change
     assert float(cache.k_scale[0, 0]) == 2.0
+
+
+def test_capturing_a_step_leaves_the_caches_as_they_are():
+    """The graph's first input may be anything; what is replayed is what counts."""
+    config = decode_step.Config(hidden=256, heads=8, kv_heads=2, head_dim=64, inner=352, layers=2, page_size=16, group=32)
+    m = decode_step.Model(config, 3, 60, seed=5)
+    cu = put([0, 5, 25, 40])
+    x = m.forward(torch.randn((40, 256), device=DEV).half(), cu)[cu[1:].long() - 1]
+    state = lambda: [t.clone().view(torch.uint8) for layer in m.layers  # noqa: E731
+                     for t in (layer.cache.k, layer.cache.v, layer.cache.k_scale, layer.cache.v_scale)] + [m.lens.clone()]
+    before = state()
+    g, at, out = m.graph(torch.full_like(x, float("inf")))
+    for a, b in zip(before, state()):
+        assert torch.equal(a, b)
+    at.copy_(x)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all() and m.lens.tolist() == [6, 21, 16]
+    m.close()
