@@ -37,6 +37,26 @@ bool overlap(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a
 Extent extent(const mi_decode_rows_t& r, int64_t tokens, int64_t heads, int64_t D) {
   return extent(r.data, 2 * ((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + D));
 }
+
+// Whether an element of a is one of b: [tokens][heads][D] rows of either.
+// Fused projections put both into one buffer, a token's heads side by side.
+bool meet(const mi_decode_rows_t& a, int64_t heads_a, const mi_decode_rows_t& b, int64_t heads_b, int64_t tokens,
+          int64_t D) {
+  if (!overlap(extent(a, tokens, heads_a, D), extent(b, tokens, heads_b, D))) return false;
+  if (tokens > 1 && (a.token_stride != b.token_stride || a.token_stride == 0)) return true;  // no fused layout
+  const int64_t S = a.token_stride, delta = ((intptr_t)b.data - (intptr_t)a.data) / 2;
+  // [0, la) of a token, and [off, off + lb) of the same one or another
+  auto touch = [&](int64_t la, int64_t off, int64_t lb) {
+    if (tokens == 1) return off < la && off + lb > 0;
+    const int64_t r = ((off % S) + S) % S;
+    return r < la || r + lb > S;
+  };
+  if (!touch((heads_a - 1) * a.head_stride + D, delta, (heads_b - 1) * b.head_stride + D)) return false;
+  for (int64_t i = 0; i < heads_a; ++i)
+    for (int64_t j = 0; j < heads_b; ++j)
+      if (touch(D, delta + j * b.head_stride - i * a.head_stride, D)) return true;
+  return false;
+}
 }  // namespace
 
 struct mi_decode_ctx {
@@ -239,10 +259,11 @@ mi_decode_status_t mi_decode_kv_append(mi_decode_handle_t h, const mi_decode_cac
     const Extent eq = extent(*q_out, batch->tokens, q_heads, D);
     if (!same && overlap(eq, extent(*q, batch->tokens, q_heads, D))) return MI_DECODE_ERR_INVALID_ARG;
     // a q turned in place may share its rows' buffer with k and v (a fused
-    // projection), between whose heads it lies; any other place may not
-    if (!same && (overlap(eq, extent(*k, batch->tokens, cache->kv_heads, D)) ||
-                  overlap(eq, extent(*v, batch->tokens, cache->kv_heads, D))))
-      return MI_DECODE_ERR_INVALID_ARG;
+    // projection), but none of their elements; any other place may not
+    for (const mi_decode_rows_t* x : {k, v})
+      if (same ? meet(*q_out, q_heads, *x, cache->kv_heads, batch->tokens, D)
+               : overlap(eq, extent(*x, batch->tokens, cache->kv_heads, D)))
+        return MI_DECODE_ERR_INVALID_ARG;
     a.q = *q;
     a.q_out = *q_out;
     a.q_heads = q_heads;

@@ -148,7 +148,8 @@ typedef struct {
  *   rot_dim: a multiple of 16, at most head_dim.  rope_rows must cover every
  *   position of the table (table_cols * page_size), else INVALID_ARG.
  *   q, q_out: [tokens][q_heads][head_dim] queries to be turned by the same
- *   angles, and where they go (may be q itself); q NULL or q_heads 0: none.
+ *   angles, and where they go (may be q itself, then also in one buffer with k
+ *   and v, but in none of their elements); q NULL or q_heads 0: none.
  * Scales.  For each page and head that receives tokens, with QMAX 127 (int8)
  * or 448 (e4m3): s' = max(s, max |x| / QMAX), where s is the page's scale if
  * the page already held tokens of the sequence and 0 if its first slot is
