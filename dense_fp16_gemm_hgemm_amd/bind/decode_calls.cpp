@@ -89,18 +89,19 @@ bool is(const at::Tensor& x, at::ScalarType t, std::initializer_list<int64_t> sh
   return x.scalar_type() == t && x.sizes() == c10::IntArrayRef(shape) && x.is_contiguous();
 }
 
-// [tokens, heads, head_dim] with a contiguous last dimension
+// [tokens, heads, head_dim] with a contiguous last dimension; the stride of a
+// dimension of one element says nothing
 mi_decode_rows_t rows(const at::Tensor& x, const char* name, int64_t heads, int64_t D, const at::Tensor& like) {
   if (x.dim() != 3 || x.size(1) != heads || x.size(2) != D)
     refuse(PyExc_ValueError, "%s must have shape [tokens, %lld, %lld]", name, (long long)heads, (long long)D);
   same_type(x, like, name);
   if (x.stride(2) != 1) refuse(PyExc_ValueError, "%s must have a contiguous last dimension", name);
-  return {x.data_ptr(), x.stride(0), x.stride(1)};
+  return {x.data_ptr(), x.size(0) > 1 ? x.stride(0) : heads * D, heads > 1 ? x.stride(1) : D};
 }
 
 const int32_t* int32s(const at::Tensor& x, const char* name, int64_t dim) {
   if (x.scalar_type() != at::kInt) refuse(PyExc_TypeError, "%s must be torch.int32, got %s", name, c10::toString(x.scalar_type()));
-  if (x.dim() != dim || (x.numel() && x.stride(dim - 1) != 1))
+  if (x.dim() != dim || (x.size(dim - 1) > 1 && x.stride(dim - 1) != 1))
     refuse(PyExc_ValueError, "%s must have %d dimension(s), the last one contiguous", name, (int)dim);
   return static_cast<const int32_t*>(x.data_ptr());
 }

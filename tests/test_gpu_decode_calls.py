@@ -131,3 +131,26 @@ def test_capturing_a_step_leaves_the_caches_as_they_are():
     torch.cuda.synchronize()
     assert torch.isfinite(out).all() and m.lens.tolist() == [6, 21, 16]
     m.close()
+
+
+def test_strides_of_single_elements_do_not_matter(d):
+    """One token, one key-value head and one sequence, cut from tensors of odd strides."""
+    cache, table, cu, q = make([50], [1], 4, 1, 64, 16, torch.int8, torch.float16, 73)
+    kv, rope = torch.randn((1, 1, 64), device=DEV).half(), decode.rope_table(table.shape[1] * 16, 64)
+    table, lens, past = table.to(DEV), put([50]), put([49])
+
+    def odd(x, *strides):
+        room = torch.zeros(x.numel() + 8, dtype=x.dtype, device=DEV)
+        y = room.as_strided(x.shape, strides)
+        return y.copy_(x)
+
+    q_out = torch.empty((1, 4, 64), device=DEV).half()
+    want = d.kv_append(cache, kv, kv, table, past, q=q, rope=rope)
+    got = d.kv_append(cache, odd(kv, 67, 3, 1), odd(kv, 5, 1, 1), odd(table, 3, 1), odd(past, 9), q=odd(q, 1, 64, 1),
+                      rope=rope, q_out=odd(q_out, 13, 64, 1))
+    assert torch.equal(got, want)
+    want = d.kv_attend(q, cache, table, lens)
+    assert torch.equal(d.kv_attend(odd(q, 7, 64, 1), cache, odd(table, 0, 1), odd(lens, 11), out=odd(q_out, 3, 64, 1)), want)
+    first = odd(table[:, :1], 6, 5)  # a table of one page
+    for a, b in zip(d.kv_read(cache, table, put([7])), d.kv_read(cache, first, odd(put([7]), 4))):
+        assert torch.equal(a, b)
