@@ -532,8 +532,7 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   const int64_t part_rows = (by_grid < by_len ? by_grid : by_len) * (rows < ROWS ? rows : ROWS);
   AttendArgs b = a;
   if (part_rows * D * 4 <= kJoinInside) b.join = nullptr;
-  attend_kernel<CODE, D, NT><<<grid, 64 * kWaves, 0, s>>>(b, (int)blocks);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = launch(attend_kernel<CODE, D, NT>, grid, 64 * kWaves, 0, s, b, (int)blocks);
   return e != hipSuccess || !b.join ? e : launch_join(b, grid, ROWS, s);
 }
 

@@ -24,11 +24,10 @@ hipError_t launch_join(const AttendArgs& a, int items, int block_rows, hipStream
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
   const dim3 grid(items, (unsigned)(((rows < block_rows ? rows : block_rows) + kRows - 1) / kRows));
   switch (a.cache.head_dim) {
-    case 64: join_kernel<64><<<grid, 256, 0, s>>>(a, block_rows); break;
-    case 128: join_kernel<128><<<grid, 256, 0, s>>>(a, block_rows); break;
-    default: join_kernel<256><<<grid, 256, 0, s>>>(a, block_rows);
+    case 64: return launch(join_kernel<64>, grid, 256, 0, s, a, block_rows);
+    case 128: return launch(join_kernel<128>, grid, 256, 0, s, a, block_rows);
+    default: return launch(join_kernel<256>, grid, 256, 0, s, a, block_rows);
   }
-  return hipGetLastError();
 }
 
 }  // namespace mid

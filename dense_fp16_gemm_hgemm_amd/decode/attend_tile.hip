@@ -433,8 +433,8 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   const int64_t stages = a.max_len / kStage + 1;
   if (splits > stages / 4) splits = stages / 4 > 0 ? stages / 4 : 1;
   if (items * splits * part_bytes(ROWS, D) > MI_DECODE_WORKSPACE_BYTES) splits = 1;
-  attend_tile_kernel<CODE, D, NW><<<(unsigned)(items * splits), 64 * NW, 0, s>>>(a, (int)blocks, (int)splits);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e =
+      launch(attend_tile_kernel<CODE, D, NW>, (unsigned)(items * splits), 64 * NW, 0, s, a, (int)blocks, (int)splits);
   return e != hipSuccess || splits == 1 ? e : launch_join(a, (int)items, ROWS, s);
 }
 

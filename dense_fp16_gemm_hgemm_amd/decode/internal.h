@@ -57,6 +57,16 @@ struct AttendArgs : KvArgs {
   int cus;    // the device's compute units
 };
 
+// Enqueues a kernel and returns its own launch's status: the runtime's last error
+// may be another call's, from before.
+template <typename... P, typename... A>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t shared, hipStream_t s, A... a) {
+  return [&](P... p) {
+    void* args[] = {&p...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, shared, s);
+  }(a...);
+}
+
 // Each enqueues its kernel for arguments that have been checked; none is empty.
 hipError_t launch_w4(const W4Args& a, hipStream_t s);
 hipError_t launch_append(const AppendArgs& a, hipStream_t s);

@@ -369,8 +369,7 @@ hipError_t append(const AppendArgs& a, hipStream_t s) {
   const int64_t items = (int64_t)a.batch.tokens * ((a.q_heads + 3) / 4) * (D / 16);
   const int64_t blocks = page_blocks + (a.q_heads ? (items + threads - 1) / threads : 0);
   if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-  append_kernel<CODE, BF16, D><<<dim3((unsigned)blocks), threads, 0, s>>>(a, (int)page_blocks);
-  return hipGetLastError();
+  return launch(append_kernel<CODE, BF16, D>, dim3((unsigned)blocks), threads, 0, s, a, (int)page_blocks);
 }
 
 template <int CODE, bool BF16>
@@ -387,8 +386,7 @@ hipError_t read(const ReadArgs& a, hipStream_t s) {
   const int64_t items = (int64_t)a.batch.tokens * a.cache.kv_heads * (a.cache.head_dim / 16);
   const int64_t x = (items + 255) / 256;
   if (x > INT32_MAX) return hipErrorInvalidConfiguration;
-  read_kernel<CODE, BF16><<<dim3((unsigned)x), 256, 0, s>>>(a);
-  return hipGetLastError();
+  return launch(read_kernel<CODE, BF16>, dim3((unsigned)x), 256, 0, s, a);
 }
 
 }  // namespace

@@ -332,8 +332,7 @@ hipError_t run(const W4Args& a, hipStream_t s) {
   int kw = each < WMAX / MW ? WMAX / MW / (int)each : 1;
   if (kw < 4 / MW) kw = 4 / MW;
   if (kw > KB) kw = KB;
-  w4_kernel<BF16, MT, NT, U, PER, R, MW, WMAX><<<grid, 64 * kw * MW, kw * MW * MT * 4096, s>>>(a);
-  return hipGetLastError();
+  return launch(w4_kernel<BF16, MT, NT, U, PER, R, MW, WMAX>, grid, 64 * kw * MW, kw * MW * MT * 4096, s, a);
 }
 
 template <bool BF16, int PER, int R>
@@ -363,8 +362,7 @@ hipError_t pick(const W4Args& a, hipStream_t s) {
   if (a.K < 8) {
     const int64_t blocks = ((int64_t)a.M * a.N + 255) / 256;
     if (blocks > INT32_MAX) return hipErrorInvalidConfiguration;
-    w4_short_kernel<BF16><<<dim3((unsigned)blocks), 256, 0, s>>>(a);
-    return hipGetLastError();
+    return launch(w4_short_kernel<BF16>, dim3((unsigned)blocks), 256, 0, s, a);
   }
   if (a.group % 128 == 0) return sized<BF16, 4>(a, s);
   if (a.group % 64 == 0 && 128 % a.group == 0) return sized<BF16, 2>(a, s);

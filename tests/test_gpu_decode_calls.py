@@ -1,4 +1,6 @@
 """Calls of the decode operators that leave arguments out, or name another stream."""
+import ctypes
+
 import pytest
 import torch
 
@@ -154,3 +156,24 @@ def test_strides_of_single_elements_do_not_matter(d):
     first = odd(table[:, :1], 6, 5)  # a table of one page
     for a, b in zip(d.kv_read(cache, table, put([7])), d.kv_read(cache, first, odd(put([7]), 4))):
         assert torch.equal(a, b)
+
+
+def test_an_earlier_error_of_the_runtime_is_not_a_calls_own(d):
+    """The last error that the runtime keeps may come from anywhere; a launch has a status of its own."""
+    with open("/proc/self/maps", encoding="utf-8") as f:
+        hip = ctypes.CDLL(next(line.split()[-1] for line in f if "libamdhip64" in line))
+    cache, table, cu, q = make([50], [1], 4, 1, 64, 16, torch.int8, torch.float16, 79)
+    w = decode.w4_quantize(torch.randn((32, 64), device=DEV).half(), 64)
+    x, y, out = torch.zeros((1, 64), device=DEV).half(), torch.ones((1, 32), device=DEV).half(), torch.empty_like(q)
+    table, lens = table.to(DEV), put([50])
+    want = d.kv_attend(q, cache, table, lens)
+    torch.cuda.synchronize()
+    try:
+        assert hip.hipSetDevice(99) != 0  # a refused call, which the runtime remembers
+        d.w4_linear(x, w.qweight, w.scales, n=32, group=64, out=y)
+        d.kv_append(cache, x.view(1, 1, 64), x.view(1, 1, 64), table, lens)
+        d.kv_attend(q, cache, table, lens, out=out)
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert torch.all(y == 0) and torch.equal(out, want)
