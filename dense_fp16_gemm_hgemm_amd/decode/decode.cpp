@@ -72,6 +72,7 @@ struct mi_decode_ctx {
 namespace {
 mi_decode_status_t done(mi_decode_ctx* h, hipError_t e) {
   if (e == hipSuccess) return MI_DECODE_OK;
+  if (e == hipErrorInvalidConfiguration) return MI_DECODE_ERR_UNSUPPORTED;  // more workgroups than a launch can have
   std::lock_guard<std::mutex> lk(h->mu);
   h->last_hip_error = (int)e;
   return MI_DECODE_ERR_HIP;

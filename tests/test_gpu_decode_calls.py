@@ -177,3 +177,12 @@ def test_an_earlier_error_of_the_runtime_is_not_a_calls_own(d):
         hip.hipGetLastError()
     torch.cuda.synchronize()
     assert torch.all(y == 0) and torch.equal(out, want)
+
+
+def test_more_rows_than_a_launch_can_have_are_unsupported(d):
+    w = decode.w4_quantize(torch.randn((1, 8), device=DEV).half(), 32)
+    x = torch.zeros((64 * 65535 + 1, 8), device=DEV).half()
+    with pytest.raises(decode.DecodeError) as e:
+        d.w4_linear(x, w.qweight, w.scales, n=1, group=32)
+    assert e.value.status == decode.MI_DECODE_ERR_UNSUPPORTED
+    assert torch.all(d.w4_linear(x[1:], w.qweight, w.scales, n=1, group=32) == 0)
