@@ -171,9 +171,12 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Ten
     if tuple(scales.shape) != (N, groups) or (zeros is not None and tuple(zeros.shape) != (N, groups)):
         raise ValueError(f"scales and zeros must have shape {(N, groups)}")
     _dtype(scales, "scales")
+    for name, x in (("codes", codes), ("zeros", zeros)):
+        if x is not None and x.numel() and not bool(((x >= 0) & (x <= 15)).all()):
+            raise ValueError(f"{name} must be 0..15")
     nb, kb = -(-N // 16), -(-K // 128)
     full = torch.zeros((nb * 16, kb * 128), dtype=torch.int64, device=codes.device)
-    full[:N, :K] = codes.to(torch.int64) & 15
+    full[:N, :K] = codes.to(torch.int64)
     e = torch.arange(8, device=codes.device)
     tiles = full.view(nb, 16, kb, 4, 4, 8) << (4 * (e // 2) + 16 * (e % 2))  # n-tile, r, k-tile, j, c, e
     words = tiles.sum(-1).permute(0, 2, 4, 1, 3).reshape(nb, kb, 64, 4)      # entry l = 16 c + r, word j

@@ -1,5 +1,6 @@
 """The decode operators' calls without a GPU: what handles and caches say of themselves."""
 import pytest
+import torch
 
 decode = pytest.importorskip("dense_fp16_gemm_hgemm_amd.decode")
 import test_decode_host as host  # noqa: E402
@@ -38,3 +39,19 @@ def test_queries_in_place_hold_no_key_and_no_value(k, v, q, status):
     """Keys and values are read by other workgroups while queries are turned."""
     with decode.Decode(inspect_only=True) as d:
         assert host.append(d.handle, k=k, v=v, q=q, q_out=q) == status
+
+
+def test_pack_takes_codes_and_zeros_of_four_bits():
+    """Numbers outside 0..15 would come back as others."""
+    codes, scales = torch.zeros((4, 64), dtype=torch.int32), torch.ones((4, 1)).half()
+    codes[1, 2] = 15
+    assert decode.w4_unpack(decode.w4_pack(codes, scales, group=64))[1, 2] == 7
+    for bad in (16, -1, 300):
+        c, z = codes.clone(), torch.full((4, 1), 8)
+        c[3, 63] = bad
+        z[2, 0] = bad
+        with pytest.raises(ValueError, match="codes"):
+            decode.w4_pack(c, scales, group=64)
+        with pytest.raises(ValueError, match="zeros"):
+            decode.w4_pack(codes, scales, z, group=64)
+    assert decode.w4_pack(codes[:0], scales[:0], group=64).qweight.shape[0] == 0
