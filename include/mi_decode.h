@@ -26,7 +26,9 @@
  *   - Page tables, lengths and offsets are read by the kernels.  A page number
  *     outside 0 .. pages-1 is never followed: tokens on it are skipped (not
  *     appended, read as zeros, not attended to).  Lengths and offsets are
- *     clamped to the table's and the token arrays' extents.
+ *     clamped to the table's and the token arrays' extents.  Rows of outputs
+ *     whose token belongs to no sequence (before cu[0], or from cu[batch] on)
+ *     are not written.
  */
 #ifndef MI_DECODE_H
 #define MI_DECODE_H
