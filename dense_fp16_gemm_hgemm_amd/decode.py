@@ -341,7 +341,9 @@ class Decode:
         """softmax(scale q k^T) v over the cache for q [tokens, q_heads, head_dim]: each
         sequence's queries are the last of its lens[b] tokens.  Without cu_q one query a
         sequence; max_q: the most that a sequence has, which saves work where it is far
-        below all queries (the default with cu_q).  scale: head_dim ** -0.5."""
+        below all queries (the default with cu_q).  scale: head_dim ** -0.5.
+        Sequences with one query each are faster in a call of their own than in one with
+        prompt pieces of many, which is planned for the longest."""
         return _done(_calls.kv_attend(self.handle, self.device, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
                                       window, sinks, scale, out,
                                       stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_attend")

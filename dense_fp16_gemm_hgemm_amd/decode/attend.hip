@@ -31,7 +31,7 @@
 //
 // Bounds: long contexts run at the rate of a large read (32 x 131149 tokens of
 // 8 heads: 1.41 ms, 6.1 TB/s), ragged ones near it (64 sequences to 16384 tokens
-// 57 us, 4.4 TB/s), short ones at their latencies (1 x 4096 tokens 12.9 us).
+// 58 us, 4.4 TB/s), short ones at their latencies (1 x 4096 tokens 12.4 us).
 #include "attend.hpp"
 
 namespace mid {
@@ -560,9 +560,12 @@ hipError_t dims_of(const AttendArgs& a, hipStream_t s) {
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
-  // us, here and there, 32 x 8 items against 4096 tokens: 64 rows of 128 channels
-  // 96 and 162, 80 rows 204 and 166; 512 rows of 256 channels 1408 and 1317,
-  // 256 rows (1 x 8 items, 8192 tokens) 62 and 70
+  // us, here and there.  32 x 8 items against 4096 tokens: 64 rows of 128 channels
+  // 94 and 117, 80 rows 196 and 120; 64 rows of 64 channels 68 and 98, 80 rows 95
+  // and 101, 128 rows 95 and 105 (2 x 8 items, 8192 tokens: 64 rows 28 and 23, 80
+  // rows 32 and 24).  256 channels, 1 x 8 items against 8192 tokens: 128 rows 42
+  // and 50, 256 rows 62 and 63, 512 rows 99 and 95; with 32 x 8 items against
+  // 4096 tokens 64 rows 194 and 280, 80 rows 313 and 280, 512 rows 1397 and 1143.
   if (rows > (a.cache.head_dim == 256 ? 511 : 64)) return launch_attend_tile(a, s);
   return a.cache.code == MI_DECODE_INT8 ? dims_of<MI_DECODE_INT8>(a, s) : dims_of<MI_DECODE_E4M3>(a, s);
 }

@@ -15,11 +15,16 @@
 //
 // Bound: each wave's chain of products, exponentials and conversions, with two
 // waves a SIMD (registers).  2 x 2048 queries of 32 heads against 8192 tokens:
-// 536 us, 900 TFLOP/s; matrix pipes busy 41 % of it.  Products with fragments
-// read just before use 600 us, page numbers and addresses per lane 567.
+// 510 to 538 us on different boards, 900 to 940 TFLOP/s; matrix pipes are busy
+// 41 % of it, vector instructions issue in 61 %, and shared memory works 41 %,
+// a third of that for bank conflicts (by their addresses, of the value writes).
+// Products with fragments read just before use 600 us, page numbers and
+// addresses per lane 567.
 //
 // Scales.  A page's value scale goes into the exponent here too, and the sum of
-// weights takes it out again once for 8 of them.
+// weights takes it out again once for 8 of them.  Each wave takes the logarithms
+// of a stage's four scales itself (528 us; taken once, by the wave that loads
+// them, before it converts, 545 to 557).
 #include "attend.hpp"
 
 namespace mid {

@@ -10,10 +10,12 @@
 // run at once (7 x 5003 x 4072: 8.1 us; with 12 waves and two rounds 11.4).
 //
 // Bounds, measured with weights that change from call to call: up to 8 tokens
-// latency and then the weights' bytes (1 x 4096 x 4096 4.8 us, of which an
-// empty launch takes 3.4; 1 x 32768 x 4096 17.7 us, 3.9 TB/s); from 32 tokens
-// the unpacking and the groups' sums, about 290 vector instructions beside 40
-// matrix ones for 128 columns (64 x 14336 x 4096 18.7 us).
+// latency and then the weights' bytes (1 x 4096 x 4096 4.7 us, of which an
+// empty launch takes 3.4; 1 x 32768 x 4096 17.3 us, 4.0 TB/s); from 32 tokens
+// each wave's chain of unpacking, products and group sums, about 290 vector
+// instructions beside 40 matrix ones for 128 columns, at two or three waves a
+// SIMD (64 x 14336 x 4096 18.2 us: vector instructions in 55 % of the busy
+// cycles, matrix pipes 28 %; two waves unpack the same codes there).
 //
 // Codes become matrix operands without arithmetic: code c placed under the
 // exponent of 16 is the number 16 + c (fp16: bits 6..9 of 0x4c00, bf16: bits
@@ -335,6 +337,11 @@ hipError_t run(const W4Args& a, hipStream_t s) {
   return launch(w4_kernel<BF16, MT, NT, U, PER, R, MW, WMAX>, grid, 64 * kw * MW, kw * MW * MT * 4096, s, a);
 }
 
+// One or two tiles of weight rows to a workgroup, by their number (us with one
+// and two, 4096 columns, groups of 128): 1 token, 512 tiles 6.2 and 6.8, 1024
+// tiles 9.4 and 9.8, 2048 tiles 18.6 and 17.0; 8 tokens, 1024 tiles 9.9 and
+// 10.0, 1376 tiles 15.7 and 15.1, 2048 tiles 22.5 and 18.3; 16 tokens, 512
+// tiles 7.7 and 7.2, 896 tiles 11.4 and 11.9, 1376 tiles 20.2 and 15.5.
 template <bool BF16, int PER, int R>
 hipError_t few(const W4Args& a, hipStream_t s) {
   const int NB = (a.N + 15) / 16;
@@ -342,6 +349,11 @@ hipError_t few(const W4Args& a, hipStream_t s) {
   return run<BF16, 1, 2, 2, PER, R, 1, R == 4 || PER == 1 ? 12 : 16>(a, s);
 }
 
+// From 17 tokens on the border is 512 tiles (us below and above it, groups of
+// 128): 32 tokens, 256 tiles 7.4 and 7.1, 512 tiles 11.0 and 8.1, 896 tiles 17.4
+// and 12.8; 64 tokens, 256 tiles 10.4 and 16.0, 512 tiles 16.5 and 16.5, 896
+// tiles 28.9 and 17.5; groups of 32 and 64 tokens, 256 tiles 11.8 and 15.7, 512
+// tiles 18.5 and 16.2.
 template <bool BF16, int PER>
 hipError_t sized(const W4Args& a, hipStream_t s) {
   const int NB = (a.N + 15) / 16;
