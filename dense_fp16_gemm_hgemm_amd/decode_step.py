@@ -78,6 +78,7 @@ class Model:
         self.table = order.view(batch, self.cols).to(torch.int32).cuda()
         self.rope = rope_table(self.cols * c.page_size, c.head_dim)
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")  # tokens in the cache
+        self.longest = 0  # the most of them, as far as the host knows: replays of a graph are not counted
         self.decode, self.gemm = Decode(), Hgemm()
 
     def close(self):
@@ -91,11 +92,15 @@ class Model:
 
     def forward(self, x, cu=None, most=None, max_len=None):
         """x [tokens, hidden]: the next tokens of every sequence, one each, or as `cu` says (`most`
-        at most, if given); they join the cache, and the layers' output for them is returned."""
+        at most, if given); they join the cache, and the layers' output for them is returned.
+        More tokens than the page table has room for are refused."""
         c, d = self.config, self.decode
         few = cu is None
         new = 1 if few else cu[1:] - cu[:-1]
         total = self.lens + new
+        longest = self.longest + 1 if few else int(total.max())
+        if longest > self.cols * c.page_size:
+            raise ValueError(f"the page table has room for {self.cols * c.page_size} tokens a sequence, not for {longest}")
         for layer in self.layers:
             qkv = self._linear(_norm(x), layer.qkv, few).view(x.shape[0], -1, c.head_dim)
             q = d.kv_append(layer.cache, qkv[:, c.heads:c.heads + c.kv_heads], qkv[:, c.heads + c.kv_heads:],
@@ -106,12 +111,14 @@ class Model:
             g = torch.nn.functional.silu(g[:, :c.inner].float()) * g[:, c.inner:].float()
             x = x + self._linear(g.half(), layer.down, few)
         self.lens.copy_(total)
+        self.longest = longest
         return x
 
     def graph(self, x):
         """forward for one token a sequence as a graph: (graph, its input, its output).  The
-        graph reads lengths and pages when it is replayed, and advances the lengths."""
-        keep, at, out = self.lens.clone(), x.clone(), None
+        graph reads lengths and pages when it is replayed, and advances the lengths: the caller
+        sees to it that they stay within the page table."""
+        keep, longest, at, out = self.lens.clone(), self.longest, x.clone(), None
         # the warm-up has no pages: x may be anything, and in the caches a large number would
         # grow the scales of pages that hold tokens already
         table, self.table = self.table, torch.full_like(self.table, -1)
@@ -120,11 +127,12 @@ class Model:
         with torch.cuda.stream(side):
             self.forward(at)
         torch.cuda.current_stream().wait_stream(side)
-        self.table = table
+        self.table, self.longest = table, longest
         self.lens.copy_(keep)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             out = self.forward(at)
+        self.longest = longest
         return g, at, out
 
 

@@ -186,3 +186,18 @@ def test_more_rows_than_a_launch_can_have_are_unsupported(d):
         d.w4_linear(x, w.qweight, w.scales, n=1, group=32)
     assert e.value.status == decode.MI_DECODE_ERR_UNSUPPORTED
     assert torch.all(d.w4_linear(x[1:], w.qweight, w.scales, n=1, group=32) == 0)
+
+
+def test_steps_past_the_page_table_are_refused():
+    """Their tokens would be skipped, and the output computed without them."""
+    config = decode_step.Config(hidden=256, heads=8, kv_heads=2, head_dim=64, inner=352, layers=1, page_size=16, group=32)
+    m = decode_step.Model(config, 2, 30, seed=7)
+    x = m.forward(torch.randn((31, 256), device=DEV).half(), put([0, 30, 31]))[[29, 30]]
+    for _ in range(2):
+        x = m.forward(x)
+    with pytest.raises(ValueError, match="32 tokens"):
+        m.forward(x)
+    with pytest.raises(ValueError, match="32 tokens"):
+        m.forward(torch.randn((33, 256), device=DEV).half(), put([0, 0, 33]))
+    assert m.lens.tolist() == [32, 3]
+    m.close()
