@@ -21,7 +21,11 @@
 // tokens by 32 channels), so the product's columns are query rows and a lane
 // holds four tokens' logits of one row: these, rounded to binary16, are in place
 // as the right operand of the second product, whose left operand are values
-// transposed with byte permutes from 8 tokens' loads.
+// transposed with byte permutes from 8 tokens' loads.  Eleven bits of a weight
+// are what an output in binary16 has, and roundings of many weights largely
+// cancel (1 x 4096 tokens in binary16: 2.5e-4 from the exact result, of which
+// the output's own rounding is 2.1e-4); as two numbers a weight would double
+// the second product.
 //
 // Codes become binary16 operands in about one instruction each: e4m3 by the
 // conversion instruction; int8 as the subnormal (code + 128) 2^-24, which is a

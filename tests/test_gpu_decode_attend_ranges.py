@@ -44,7 +44,7 @@ def attend(q, cache, table, lens, cu):
             z = (x @ kh.t() * D ** -0.5).masked_fill(~seen, -math.inf)
             size = (x.abs() @ kh.abs().t() * D ** -0.5).masked_fill(~seen, 0).amax(1, keepdim=True)
             w = torch.softmax(z, -1)
-            most = (w * cache.v_scale[page, h // G].to(F)).amax(1, keepdim=True) * QMAX[cache.v.dtype]
+            most = (w * cache.v_scale[page, h // G].abs().to(F)).amax(1, keepdim=True) * QMAX[cache.v.dtype]
             out[cu[b]:cu[b + 1], h] = w @ vh
             bound[cu[b]:cu[b + 1], h] = ((2.0 ** -11 + 2.0 ** -17 + 2 * size * (D + 8) * 2.0 ** -24) * (w @ vh.abs())
                                          + seen.sum(1, keepdim=True) * 2.0 ** -25 * most)
@@ -95,6 +95,21 @@ def test_very_small_and_very_large_values(d, D, G, new, size, codes):
     lens, page = [300 + new], 32
     cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], torch.bfloat16, 35)
     cache.v_scale.mul_(size)
+    got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
+    check(got, *attend(q, cache, table, lens, cu))
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("D, G, new", ROWS)
+def test_negative_zero_and_tiny_scales(d, D, G, new, codes):
+    """A value is its code times its scale, whatever the scale's sign; some pages hold zeros, or nearly."""
+    lens, page = [700 + new], 16
+    cache, table, cu, q = make(lens, [new], G, 1, D, page, CODES[codes], torch.bfloat16, 37)
+    order = table[0, :-(-lens[0] // page)].long().to(DEV)
+    cache.v_scale[order[::2]] *= -1
+    cache.k_scale[order[::3]] *= -1
+    cache.v_scale[order[5::7]] = 0
+    cache.v_scale[order[6::7]] *= 2.0 ** -100
     got = d.kv_attend(q, cache, table.to(DEV), put(lens), put(cu), new)
     check(got, *attend(q, cache, table, lens, cu))
 
