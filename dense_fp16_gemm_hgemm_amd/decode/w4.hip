@@ -26,10 +26,9 @@
 // Both products are exact in binary32 and the offset at most doubles to
 // quadruples the terms' size, so this costs about two of binary32's 24 bits.
 // Where x is infinite, or the offset takes a sum past binary32, the difference
-// is NaN: a row of a workgroup's results that are not all finite is summed
-// again, term by term, by all its threads (1 x 4096 x 4096 with a NaN 17 us, 64
-// x 14336 x 4096 with one such row 72; by the thread that has the result 266
-// and 341).
+// is NaN: results that are not finite are summed again, term by term, by the
+// wave that has them, unless x holds a NaN (1 x 4096 x 4096 4.5 us, with a NaN
+// 7.2, with an infinity 60; 64 x 14336 x 4096 with one such row 18.9, 21.5, 76).
 #include "device.hpp"
 
 namespace mid {
@@ -70,25 +69,54 @@ __device__ inline void wave_shared() {
 }
 
 // sum_k x[m][k] ((c - z) s), one term after the other, over every step-th word
-// of eight columns.
+// of eight columns; the loads of four words are in flight at a time.
 template <bool BF16>
 __device__ inline float sum_terms(const W4Args& p, int64_t m, int n, int first, int step) {
+  constexpr int DEPTH = 4;
   const uint16_t* x = static_cast<const uint16_t*>(p.x) + m * p.ldx;
   const uint16_t* scales = static_cast<const uint16_t*>(p.scales) + n;
   const int64_t np = (int64_t)((p.N + 15) >> 4) * 16;
   const uint32_t* tiles = p.qw + (int64_t)(n >> 4) * ((p.K + 127) >> 7) * 256 + 4 * (n & 15);
+  const int words = (p.K + 7) >> 3;
   float y = 0.f;
-  for (int k0 = 8 * first; k0 < p.K; k0 += 8 * step) {
-    const uint32_t w = tiles[(int64_t)(k0 >> 7) * 256 + (k0 >> 3 & 3) * 64 + (k0 >> 5 & 3)];
-    const int64_t at = k0 / p.group * np;
-    const float s = from16<BF16>(scales[at]);
-    const int z = p.zeros ? p.zeros[at + n] : 8;
+  for (int at = first; at < words; at += DEPTH * step) {
+    uint32_t w[DEPTH];
+    uint16_t s[DEPTH], v[DEPTH][8];
+    int z[DEPTH];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k0 + e < p.K)
-        y = __builtin_fmaf(from16<BF16>(x[k0 + e]), (float)((int)(w >> (4 * (e / 2) + 16 * (e % 2)) & 15) - z) * s, y);
+    for (int d = 0; d < DEPTH; ++d) {
+      const int k0 = 8 * min(at + d * step, words - 1);
+      const int64_t group = k0 / p.group * np;
+      w[d] = tiles[(int64_t)(k0 >> 7) * 256 + (k0 >> 3 & 3) * 64 + (k0 >> 5 & 3)];
+      s[d] = scales[group];
+      z[d] = p.zeros ? p.zeros[group + n] : 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[d][e] = x[min(k0 + e, p.K - 1)];
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * (at + d * step) + e < p.K)
+          y = __builtin_fmaf(from16<BF16>(v[d][e]),
+                             (float)((int)(w[d] >> (4 * (e / 2) + 16 * (e % 2)) & 15) - z[d]) * from16<BF16>(s[d]), y);
   }
   return y;
+}
+
+// Whether row m of x holds a NaN, by a whole wave: its results are NaN then.
+template <bool BF16>
+__device__ inline bool has_nan(const W4Args& p, int64_t m, int lane) {
+  const uint16_t* x = static_cast<const uint16_t*>(p.x) + m * p.ldx;
+  bool nan = false;
+  for (int k0 = lane; k0 < p.K; k0 += 8 * 64) {
+    uint16_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x[min(k0 + 64 * e, p.K - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nan |= (v[e] & 0x7fff) > (BF16 ? 0x7f80 : 0x7c00);
+  }
+  return __any(nan);
 }
 
 // MT x NT tiles of 16 tokens by 16 rows of weights to a wave, U blocks of 128
@@ -251,62 +279,45 @@ __global__ __launch_bounds__(64 * WMAX) void w4_kernel(W4Args p) {
   // red[kw][mw][m][t][lane] as 4 tokens each; summed in the order of kw
   constexpr int PART = MT * NT * 64;
   f32x4* part = reinterpret_cast<f32x4*>(red);
-  __shared__ uint32_t again[2];  // rows of the workgroup, 64 at most, with a sum that is not finite
-  if (threadIdx.x < 2) again[threadIdx.x] = 0;
   __syncthreads();  // every wave is done with its piece
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < NT; ++t) part[wave * PART + (m * NT + t) * 64 + lane] = total[m][t];
-  float odd = 0.f;  // NaN if one of the lane's sums is not finite; scales past N may be anything
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) odd = __builtin_fmaf((nb0 + t) * 16 + r < p.N ? total[m][t][e] : 0.f, 0.f, odd);
-  if (odd != 0.f) {
-    for (int m = 0; m < MT; ++m)
-      for (int e = 0; e < 4; ++e) {
-        const int at = (mw * MT + m) * 16 + c * 4 + e;
-        bool bad = false;
-        for (int t = 0; t < NT; ++t) bad |= (nb0 + t) * 16 + r < p.N && !(fabsf(total[m][t][e]) < INFINITY);
-        if (bad) atomicOr(&again[at >> 5], 1u << (at & 31));
-      }
-  }
   __syncthreads();
   // thread -> (mw, m, t, l): lanes of 16 neighbours hold 16 neighbouring columns of four tokens
   for (int i = threadIdx.x; i < MW * PART; i += blockDim.x) {
     f32x4 y = part[i];
     for (int w = 1; w < KW; ++w) y += part[w * MW * PART + i];
     const int l = i & 63, t = (i >> 6) % NT, m = (i >> 6) / NT;  // m counts over the MW waves' tiles
-    const int n = (nb0 + t) * 16 + (l & 15);
+    const int n = (nb0 + t) * 16 + (l & 15), row0 = blockIdx.y * (16 * MT * MW) + m * 16;
+    float odd = 0.f;  // NaN if one of the four is not finite; scales past N may be anything
+#pragma unroll
+    for (int e = 0; e < 4; ++e) odd = __builtin_fmaf(y[e], 0.f, odd);
+    if (__any(n < p.N && odd != 0.f)) {
+      // the wave takes one token after the other: 16 columns, a quarter of K to a lane
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool bad = n < p.N && !(fabsf(y[e]) < INFINITY);
+        const uint64_t where = __ballot(bad);
+        for (int q = 0; q < 4; ++q) {
+          const int row = row0 + 4 * q + e;
+          if ((where >> (16 * q) & 0xffff) == 0 || row >= p.M || has_nan<BF16>(p, row, l)) continue;
+          float sum = n < p.N ? sum_terms<BF16>(p, row, n, l >> 4, 4) : 0.f;
+          sum += __shfl_xor(sum, 16);
+          sum += __shfl_xor(sum, 32);
+          if (bad && (l >> 4) == q) y[e] = sum;
+        }
+      }
+    }
     if (n >= p.N) continue;
     const float b = p.bias ? from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]) : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int row = blockIdx.y * (16 * MT * MW) + m * 16 + (l >> 4) * 4 + e;
+      const int row = row0 + (l >> 4) * 4 + e;
       if (row < p.M) static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(y[e] + b);
     }
   }
-  if ((again[0] | again[1]) == 0) return;
-  __syncthreads();
-  constexpr int COLS = 16 * NT;
-  const int tid = threadIdx.x, n = nb0 * 16 + tid % COLS;
-  for (int half = 0; half < 2; ++half)
-    for (uint32_t left = again[half]; left; left &= left - 1) {
-      const int64_t row = blockIdx.y * (16 * MT * MW) + 32 * half + __builtin_ctz(left);
-      if (row >= p.M) break;  // the last row of x once more
-      red[tid] = n < p.N ? sum_terms<BF16>(p, row, n, tid / COLS, blockDim.x / COLS) : 0.f;
-      __syncthreads();
-      if (tid < COLS && n < p.N) {
-        float y = red[tid];
-        for (int i = tid + COLS; i < (int)blockDim.x; i += COLS) y += red[i];
-        if (p.bias) y += from16<BF16>(static_cast<const uint16_t*>(p.bias)[n]);
-        static_cast<uint16_t*>(p.y)[row * p.ldy + n] = to16<BF16>(y);
-      }
-      __syncthreads();
-    }
 }
 
 // K below 8, where no whole piece of a row exists: one result to a thread.
