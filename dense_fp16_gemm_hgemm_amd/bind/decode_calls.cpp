@@ -204,9 +204,9 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// handle, its device, cache, device, k, v, table, past, cu_new, max_new, q, rope, interleaved, q_out, stream
+// handle, its device, cache, device, k, v, table, past, cu_new, max_new, q, rope, interleaved, q_out, stream, positions
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call(n_args, 15, [&]() -> PyObject* {
+  return call(n_args, 16, [&]() -> PyObject* {
     const mi_decode_cache_t& c = cache_of(a[2]);
     const c10::Device device = device_of(a[3]);
     same_device(a[1], device);
@@ -234,7 +234,11 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     }
     if (rope && (rope->scalar_type() != at::kFloat || rope->dim() != 2 || !rope->is_contiguous()))
       refuse(PyExc_ValueError, "rope must be a contiguous float32 [positions, rot_dim] table");
-    if (rope && rope->size(0) < (int64_t)t.table_cols * c.page_size)
+    const at::Tensor* positions = maybe(a[15], "positions");
+    const int32_t* turned = positions ? int32s(*positions, "positions", 1) : nullptr;
+    if (positions && positions->size(0) != T) refuse(PyExc_ValueError, "positions must have one entry a token (%lld), got %lld", (long long)T, (long long)positions->size(0));
+    on(positions, device, "positions");
+    if (rope && !positions && rope->size(0) < (int64_t)t.table_cols * c.page_size)
       refuse(PyExc_ValueError, "rope has %lld positions, the table has %lld", (long long)rope->size(0), (long long)t.table_cols * c.page_size);
     on(&k, device, "k");
     on(&v, device, "v");
@@ -243,9 +247,9 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(rope, device, "rope");
     const int on_pairs = PyObject_IsTrue(a[12]);
     if (on_pairs < 0) throw Refused{};
-    const mi_decode_status_t st = mi_decode_kv_append(
+    const mi_decode_status_t st = mi_decode_kv_append_at(
         handle(a[0]), &c, type, &t, &rk, &rv, rope ? static_cast<const float*>(rope->data_ptr()) : nullptr,
-        rope ? rope->size(0) : 0, rope ? (int32_t)rope->size(1) : 0, on_pairs, (int32_t)hq, q ? &rq : nullptr,
+        rope ? rope->size(0) : 0, rope ? (int32_t)rope->size(1) : 0, on_pairs, turned, (int32_t)hq, q ? &rq : nullptr,
         q ? &ro : nullptr, stream.raw);
     if (st != MI_DECODE_OK || q) return result(st, q ? *q_out : k);
     Py_RETURN_NONE;
@@ -275,9 +279,10 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// handle, its device, cache, device, q, table, lens, cu_q, max_q, max_len, window, sinks, scale, out, stream
-PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
-  return call(n_args, 15, [&]() -> PyObject* {
+// handle, its device, cache, device, q, table, lens, cu_q, max_q, max_len, window, sinks, scale, out, stream,
+// and for a tree: seen
+PyObject* attend(PyObject* const* a, Py_ssize_t n_args, bool tree) {
+  return call(n_args, tree ? 16 : 15, [&]() -> PyObject* {
     const mi_decode_cache_t& c = cache_of(a[2]);
     const c10::Device device = device_of(a[3]);
     same_device(a[1], device);
@@ -305,13 +310,166 @@ PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const mi_decode_rows_t ro = rows(*out, "out", hq, c.head_dim, q);
     on(&q, device, "q");
     on(out, device, "out");
-    return result(mi_decode_kv_attend(handle(a[0]), &c, type, &t, max_len, (int32_t)hq, &rq, &ro, (float)scale, window, sinks,
-                                      stream.raw), *out);
+    if (!tree)
+      return result(mi_decode_kv_attend(handle(a[0]), &c, type, &t, max_len, (int32_t)hq, &rq, &ro, (float)scale, window, sinks,
+                                        stream.raw), *out);
+    const at::Tensor& seen = *tensor(a[15], "seen");
+    const int32_t* bits = int32s(seen, "seen", 2);
+    const int64_t words = seen.size(1);
+    if (seen.size(0) != T) refuse(PyExc_ValueError, "seen must have one row a token (%lld), got %lld", (long long)T, (long long)seen.size(0));
+    if (words > INT32_MAX || (T > 0 && words * 32 < t.max_tokens))
+      refuse(PyExc_ValueError, "seen has %lld words of 32 bits a token, too few for max_q=%d", (long long)words, t.max_tokens);
+    on(&seen, device, "seen");
+    return result(mi_decode_kv_attend_tree(handle(a[0]), &c, type, &t, max_len, (int32_t)hq, &rq, &ro, bits,
+                                           T > 1 ? seen.stride(0) : words, (int32_t)words, (float)scale, window, sinks,
+                                           stream.raw), *out);
+  });
+}
+PyObject* kv_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) { return attend(a, n_args, false); }
+PyObject* kv_attend_tree(PyObject*, PyObject* const* a, Py_ssize_t n_args) { return attend(a, n_args, true); }
+
+// handle, its device, cache, device, table, past, keep, cu, max_keep, stream
+PyObject* kv_keep(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return call(n_args, 10, [&]() -> PyObject* {
+    const mi_decode_cache_t& c = cache_of(a[2]);
+    const c10::Device device = device_of(a[3]);
+    same_device(a[1], device);
+    const OnStream stream(a[9], device);
+    const at::Tensor& keep = *tensor(a[6], "keep");
+    const int32_t* of = int32s(keep, "keep", 1);
+    const int64_t T = keep.size(0);
+    const mi_decode_batch_t t = batch_of(a[4], a[5], a[7], T, longest(a[8], a[7], T, "max_keep"), device, "past", "cu_keep");
+    on(&keep, device, "keep");
+    const mi_decode_status_t st = mi_decode_kv_keep(handle(a[0]), &c, &t, of, stream.raw);
+    if (st != MI_DECODE_OK) return PyLong_FromLong(st);
+    Py_RETURN_NONE;
   });
 }
 
+// handle, its device, cache, device, src, dst, stream
+PyObject* kv_copy(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return call(n_args, 7, [&]() -> PyObject* {
+    const mi_decode_cache_t& c = cache_of(a[2]);
+    const c10::Device device = device_of(a[3]);
+    same_device(a[1], device);
+    const OnStream stream(a[6], device);
+    const at::Tensor &src = *tensor(a[4], "src"), &dst = *tensor(a[5], "dst");
+    const int32_t *from = int32s(src, "src", 1), *to = int32s(dst, "dst", 1);
+    if (src.size(0) != dst.size(0))
+      refuse(PyExc_ValueError, "src and dst must have the same length, got %lld and %lld", (long long)src.size(0), (long long)dst.size(0));
+    on(&src, device, "src");
+    on(&dst, device, "dst");
+    const mi_decode_status_t st = mi_decode_kv_copy(handle(a[0]), &c, from, to, src.size(0), stream.raw);
+    if (st != MI_DECODE_OK) return PyLong_FromLong(st);
+    Py_RETURN_NONE;
+  });
+}
+
+// 2-D with unit-stride rows; the distance of rows says nothing where there is one
+int64_t row_distance(const at::Tensor& x, const char* name, at::ScalarType type, int64_t rows, int64_t cols) {
+  if (x.scalar_type() != type) refuse(PyExc_TypeError, "%s must be %s, got %s", name, c10::toString(type), c10::toString(x.scalar_type()));
+  if (x.dim() != 2 || x.size(0) != rows || x.size(1) != cols || (cols > 1 && x.stride(1) != 1))
+    refuse(PyExc_ValueError, "%s must have shape (%lld, %lld) and unit-stride rows", name, (long long)rows, (long long)cols);
+  return rows > 1 ? x.stride(0) : cols;
+}
+int64_t row_distance(const at::Tensor& x, const char* name) {
+  return row_distance(x, name, x.scalar_type(), x.dim() == 2 ? x.size(0) : 0, x.dim() == 2 ? x.size(1) : 0);
+}
+const void* vector(const at::Tensor* x, const char* name, at::ScalarType type, int64_t n) {
+  if (!x) return nullptr;
+  if (x->scalar_type() != type) refuse(PyExc_TypeError, "%s must be %s, got %s", name, c10::toString(type), c10::toString(x->scalar_type()));
+  if (x->dim() != 1 || x->size(0) != n || (n > 1 && x->stride(0) != 1))
+    refuse(PyExc_ValueError, "%s must be contiguous with %lld entries", name, (long long)n);
+  return x->data_ptr();
+}
+
+// handle, its device, x, weight, residual, eps, codes, scales, total, stream
+PyObject* rms_norm_f8(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return call(n_args, 10, [&]() -> PyObject* {
+    const at::Tensor& x = *tensor(a[2], "x");
+    const at::Tensor *weight = maybe(a[3], "weight"), *residual = maybe(a[4], "residual");
+    const mi_decode_dtype_t type = type16(x, "x");
+    if (!x.is_cuda()) refuse(PyExc_ValueError, "x must be on the GPU");
+    same_device(a[1], x.device());
+    const OnStream stream(a[9], x.device());
+    const int64_t ldx = row_distance(x, "x"), M = x.size(0), K = x.size(1), blocks = (K + 127) / 128;
+    const int64_t ldr = residual ? row_distance(*residual, "residual", x.scalar_type(), M, K) : 0;
+    const void* g = vector(weight, "weight", x.scalar_type(), K);
+    const double eps = PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) throw Refused{};
+    const at::Tensor *codes = maybe(a[6], "codes"), *scales = maybe(a[7], "scales"), *total = maybe(a[8], "total");
+    if (total && !residual) refuse(PyExc_ValueError, "without a residual there is no total");
+    at::Tensor made[3];
+    auto ready = [&](const at::Tensor*& out, int i, at::ScalarType t, int64_t cols) {
+      if (out) return;
+      made[i] = at::empty({M, cols}, x.options().dtype(t));
+      out = &made[i];
+    };
+    ready(codes, 0, at::kFloat8_e4m3fn, K);
+    ready(scales, 1, at::kFloat, blocks);
+    if (residual) ready(total, 2, x.scalar_type(), K);
+    const int64_t ldc = row_distance(*codes, "codes", at::kFloat8_e4m3fn, M, K);
+    const int64_t lds = row_distance(*scales, "scales", at::kFloat, M, blocks);
+    const int64_t ldt = total ? row_distance(*total, "total", x.scalar_type(), M, K) : 0;
+    on(weight, x.device(), "weight");
+    on(residual, x.device(), "residual");
+    on(codes, x.device(), "codes");
+    on(scales, x.device(), "scales");
+    on(total, x.device(), "total");
+    const mi_decode_status_t st = mi_decode_rms_norm_f8(
+        handle(a[0]), type, M, K, x.data_ptr(), ldx, residual ? residual->data_ptr() : nullptr, ldr, g, (float)eps,
+        codes->data_ptr(), ldc, static_cast<float*>(scales->data_ptr()), lds, total ? total->data_ptr() : nullptr, ldt,
+        stream.raw);
+    if (st != MI_DECODE_OK) return PyLong_FromLong(st);
+    PyObject *pc = THPVariable_Wrap(*codes), *ps = THPVariable_Wrap(*scales);
+    PyObject* pt = total ? THPVariable_Wrap(*total) : Py_NewRef(Py_None);
+    PyObject* all = pc && ps && pt ? PyTuple_Pack(3, pc, ps, pt) : nullptr;
+    Py_XDECREF(pc);
+    Py_XDECREF(ps);
+    Py_XDECREF(pt);
+    return all;
+  });
+}
+
+// handle, its device, x, x_scales, weight, w_scales, bf16, bias, out, stream
+PyObject* f8_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return call(n_args, 10, [&]() -> PyObject* {
+    const at::Tensor &x = *tensor(a[2], "x"), &xs = *tensor(a[3], "x_scales"), &w = *tensor(a[4], "weight"), &ws = *tensor(a[5], "w_scales");
+    const at::Tensor* bias = maybe(a[7], "bias");
+    if (x.scalar_type() != at::kFloat8_e4m3fn) refuse(PyExc_TypeError, "x must be torch.float8_e4m3fn, got %s", c10::toString(x.scalar_type()));
+    if (!x.is_cuda()) refuse(PyExc_ValueError, "x must be on the GPU");
+    same_device(a[1], x.device());
+    const OnStream stream(a[9], x.device());
+    const int bf16 = PyObject_IsTrue(a[6]);
+    const at::ScalarType type = bf16 ? at::kBFloat16 : at::kHalf;
+    const int64_t ldx = row_distance(x, "x"), M = x.size(0), K = x.size(1), kb = (K + 127) / 128;
+    const int64_t N = w.dim() == 2 ? w.size(0) : 0, ldw = row_distance(w, "weight", at::kFloat8_e4m3fn, N, K);
+    const int64_t ldxs = row_distance(xs, "x_scales", at::kFloat, M, kb);
+    const int64_t ldws = row_distance(ws, "w_scales", at::kFloat, (N + 127) / 128, kb);
+    const void* b = vector(bias, "bias", type, N);
+    at::Tensor made;
+    const at::Tensor* out = maybe(a[8], "out");
+    if (!out) {
+      made = at::empty({M, N}, x.options().dtype(type));
+      out = &made;
+    }
+    const int64_t ldy = row_distance(*out, "out", type, M, N);
+    on(&xs, x.device(), "x_scales");
+    on(&w, x.device(), "weight");
+    on(&ws, x.device(), "w_scales");
+    on(bias, x.device(), "bias");
+    on(out, x.device(), "out");
+    return result(mi_decode_f8_linear(handle(a[0]), bf16 ? MI_DECODE_BF16 : MI_DECODE_F16, M, N, K, x.data_ptr(), ldx,
+                                      static_cast<const float*>(xs.data_ptr()), ldxs, w.data_ptr(), ldw,
+                                      static_cast<const float*>(ws.data_ptr()), ldws, b, out->data_ptr(), ldy, stream.raw),
+                  *out);
+  });
+}
+
+
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(w4_linear), FAST(kv_append), FAST(kv_read), FAST(kv_attend), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(w4_linear), FAST(kv_append), FAST(kv_read), FAST(kv_attend),
+                         FAST(kv_attend_tree), FAST(kv_keep), FAST(kv_copy), FAST(rms_norm_f8), FAST(f8_linear), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

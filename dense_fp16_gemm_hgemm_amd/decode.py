@@ -1,5 +1,7 @@
 """Binding of libmi_decode: the operators beside the projections of a decode step.
 
+One token a sequence:
+
 * ``Decode.w4_linear``  -- linear layer with 4-bit weights and group scales, for few tokens;
 * ``Decode.kv_append``  -- keys and values of new tokens, rotated by their positions, into a
   paged 8-bit cache with a scale for each page and head;
@@ -7,14 +9,25 @@
 * ``Decode.kv_attend``  -- attention over that cache (grouped heads, causal, a window with
   first tokens that stay visible), one query a sequence or ragged many.
 
+Several drafted continuations of each sequence, verified at once:
+
+* ``Decode.rms_norm_f8``    -- norm with the residual's addition, into 8-bit floats with a scale
+  for 128 columns;
+* ``Decode.f8_linear``      -- linear layer of 8-bit floats with block scales, for any number of
+  tokens;
+* ``Decode.kv_append``      -- with ``positions``, as drafted tokens do not stand where they lie;
+* ``Decode.kv_attend_tree`` -- attention in which a drafted token sees the context and its branch;
+* ``Decode.kv_keep``        -- the accepted tokens move together;
+* ``Decode.kv_copy``        -- copies of pages, for conversations that go on from the same tokens.
+
 Operations, layouts and rules are those of ``include/mi_decode.h``; torch supplies device
-memory and the stream.  The four calls check and marshal their arguments in an extension
+memory and the stream.  The calls check and marshal their arguments in an extension
 module (``bind/decode_calls.cpp``), because a decode step's kernels take microseconds; the
 rest of the library is reached with ctypes.  A call returns
 without synchronising, and every call may be captured into a graph.  Work goes to the
 current stream, or to ``stream`` (a torch stream, or a handle as an integer), whose memory
-the results are then, as if it were the current one.  ``kv_attend`` uses the
-handle's workspace: calls that may overlap on different streams need handles of their own.
+the results are then, as if it were the current one.  ``kv_attend`` and ``kv_attend_tree`` use
+the handle's workspace: calls that may overlap on different streams need handles of their own.
 
     from dense_fp16_gemm_hgemm_amd import decode
     d = decode.Decode()
@@ -23,6 +36,14 @@ handle's workspace: calls that may overlap on different streams need handles of 
     cache = decode.KvCache.empty(pages, kv_heads, head_dim, page_size=64)
     q = d.kv_append(cache, k, v, table, past, q=q, rope=decode.rope_table(max_len, head_dim))
     o = d.kv_attend(q, cache, table, past + 1, max_len=max_len)
+
+    w8 = decode.f8_quantize(weight)                      # [N, K] -> F8 (weight, scales)
+    seen, depth = decode.tree(parents)                   # of one sequence's drafted tokens
+    c, s, x = d.rms_norm_f8(x, norm_weight, residual)
+    y = d.f8_linear(c, s, w8.weight, w8.scales)
+    q = d.kv_append(cache, k, v, table, past, cu, q=q, rope=rope, positions=past + depth)
+    o = d.kv_attend_tree(q, cache, table, past + drafts, seen, cu)
+    d.kv_keep(cache, table, past, path, cu_path)         # then past += len(path)
 
 ``python -m dense_fp16_gemm_hgemm_amd.decode_step`` runs them together.
 """
@@ -35,7 +56,7 @@ from typing import NamedTuple, Optional
 import torch  # imported first so that both use one HIP runtime
 
 __all__ = ["Decode", "DecodeError", "KvCache", "W4", "w4_pack", "w4_unpack", "w4_quantize",
-           "rope_table", "LIB_PATH"]
+           "F8", "f8_quantize", "f8_values", "tree", "rope_table", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmi_decode.so")
 if not os.path.exists(LIB_PATH):
@@ -92,6 +113,17 @@ _kv_append = _sig("mi_decode_kv_append", ctypes.c_int, _p, _p, ctypes.c_int, _p,
 _kv_read = _sig("mi_decode_kv_read", ctypes.c_int, _p, _p, ctypes.c_int, _p, _p, _p, _p)
 _kv_attend = _sig("mi_decode_kv_attend", ctypes.c_int, _p, _p, ctypes.c_int, _p, _i64, _i32, _p, _p,
                   _f32, _i32, _i32, _p)
+
+_kv_append_at = _sig("mi_decode_kv_append_at", ctypes.c_int, _p, _p, ctypes.c_int, _p, _p, _p, _p, _i64,
+                     _i32, _i32, _p, _i32, _p, _p, _p)
+_kv_attend_tree = _sig("mi_decode_kv_attend_tree", ctypes.c_int, _p, _p, ctypes.c_int, _p, _i64, _i32, _p, _p,
+                       _p, _i64, _i32, _f32, _i32, _i32, _p)
+_kv_keep = _sig("mi_decode_kv_keep", ctypes.c_int, _p, _p, _p, _p, _p)
+_kv_copy = _sig("mi_decode_kv_copy", ctypes.c_int, _p, _p, _p, _p, _i64, _p)
+_rms_norm_f8 = _sig("mi_decode_rms_norm_f8", ctypes.c_int, _p, ctypes.c_int, _i64, _i64, _p, _i64, _p, _i64, _p,
+                    _f32, _p, _i64, _p, _i64, _p, _i64, _p)
+_f8_linear = _sig("mi_decode_f8_linear", ctypes.c_int, _p, ctypes.c_int, _i64, _i64, _i64, _p, _i64, _p, _i64,
+                  _p, _i64, _p, _i64, _p, _p, _i64, _p)
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _CODES = {torch.int8: 0, torch.float8_e4m3fn: 1}
@@ -220,6 +252,66 @@ def w4_quantize(weight: torch.Tensor, group: int = 128, symmetric: bool = True) 
     return w4_pack(codes, s, zeros, group)
 
 
+# -------------------------------------------------------- 8-bit floats --
+
+class F8(NamedTuple):
+    """Weights in 8-bit floats for ``Decode.f8_linear``: a value is its code times the scale of
+    its 128 rows and 128 columns."""
+    weight: torch.Tensor    # float8_e4m3fn [N, K]
+    scales: torch.Tensor    # float32 [ceil(N / 128), ceil(K / 128)]
+
+
+def f8_quantize(weight: torch.Tensor) -> F8:
+    """[N, K] weights of any floating type: for each 128 rows and 128 columns the scale that takes
+    the largest magnitude to 448."""
+    if weight.dim() != 2 or not weight.is_floating_point():
+        raise ValueError("weight must be [N, K] of a floating type")
+    N, K = weight.shape
+    nb, kb = -(-N // 128), -(-K // 128)
+    w = torch.zeros((nb * 128, kb * 128), device=weight.device)
+    w[:N, :K] = weight.float()
+    w = w.view(nb, 128, kb, 128)
+    s = w.abs().amax((1, 3)) / 448
+    at = s[:, None, :, None]
+    codes = torch.where(at == 0, torch.zeros_like(w), w / at).clamp(-448, 448)  # a NaN stays one
+    return F8(codes.view(nb * 128, kb * 128)[:N, :K].to(torch.float8_e4m3fn).contiguous(), s)
+
+
+def f8_values(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """float32 values of codes [rows, K] with a scale for 128 columns of each row, as activations
+    have them, or of 128 rows, as weights do."""
+    rows, K = codes.shape
+    kb = -(-K // 128)
+    if tuple(scales.shape) not in ((rows, kb), (-(-rows // 128), kb)):
+        raise ValueError(f"scales must have shape {(rows, kb)} or {(-(-rows // 128), kb)}")
+    if scales.shape[0] != rows:
+        scales = scales.repeat_interleave(128, 0)[:rows]
+    return codes.float() * scales.repeat_interleave(128, 1)[:, :K]
+
+
+# ------------------------------------------------------- drafted tokens --
+
+def tree(parents):
+    """What drafted tokens see, from their parents.
+
+    ``parents``: for each of a sequence's drafted tokens the index of the one that it continues,
+    an earlier one, or -1 where it continues the sequence itself.  Returns, on the CPU, ``seen``
+    int32 [tokens, words] for ``Decode.kv_attend_tree`` (a token sees its ancestors and itself)
+    and ``depth`` int32 [tokens], how far a token stands behind the sequence."""
+    parents = [int(p) for p in parents]
+    n = len(parents)
+    bits, depth = [], []
+    for i, p in enumerate(parents):
+        if not -1 <= p < i:
+            raise ValueError(f"parents[{i}] must be -1 or an earlier token, got {p}")
+        bits.append((bits[p] if p >= 0 else 0) | 1 << i)
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    words = -(-n // 32)
+    seen = [[(b >> 32 * w & 0xffffffff) for w in range(words)] for b in bits]
+    seen = torch.tensor(seen, dtype=torch.int64).view(n, words)
+    return torch.where(seen >= 2 ** 31, seen - 2 ** 32, seen).to(torch.int32), torch.tensor(depth, dtype=torch.int32)
+
+
 def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """float32 [positions, rot_dim]: cosines, then sines, of position * base^(-2 i / rot_dim),
     with the angles in float64."""
@@ -313,13 +405,16 @@ class Decode:
                      "mi_decode_w4_linear")
 
     def kv_append(self, cache, k, v, table, past, cu_new=None, max_new=None, *, q=None, rope=None,
-                  interleaved=False, q_out=None, stream=None):
+                  interleaved=False, q_out=None, positions=None, stream=None):
         """Append k and v [tokens, kv_heads, head_dim] after the `past` tokens of each sequence;
         returns q [tokens, q_heads, head_dim] turned by its positions (None without q).
+        positions: int32 [tokens], the rows of rope that keys and queries are turned by, where
+        these are not the tokens' places in the cache (drafted tokens).
         Without cu_new one token a sequence; max_new: the most that a sequence has of them,
         which saves work where it is far below all tokens (the default with cu_new)."""
         return _done(_calls.kv_append(self.handle, self.device, cache._at, cache._dev, k, v, table, past, cu_new, max_new, q, rope,
-                                      interleaved, q_out, stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_append")
+                                      interleaved, q_out, stream if stream is None else _raw(stream, cache.device), positions),
+                     "mi_decode_kv_append_at")
 
     def kv_read(self, cache, table, start, cu=None, *, tokens=None, max_tokens=None, dtype=torch.float16,
                 stream=None):
@@ -347,3 +442,47 @@ class Decode:
         return _done(_calls.kv_attend(self.handle, self.device, cache._at, cache._dev, q, table, lens, cu_q, max_q, max_len,
                                       window, sinks, scale, out,
                                       stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_attend")
+
+    def kv_attend_tree(self, q, cache, table, lens, seen, cu_q=None, max_q=None, *, max_len=None, window=0, sinks=0,
+                       scale=None, out=None, stream=None):
+        """kv_attend for drafted tokens, which are the last of each sequence's lens[b] tokens: bit
+        a % 32 of seen[t, a // 32] (int32 [tokens, words]) says whether token t of the call sees
+        its sequence's drafted token a (``tree`` makes them).  Of the tokens before the drafts it
+        sees all, or those of a window: the last `window` ones up to its own position, which is
+        behind them by the number of drafted tokens that it sees besides itself, and the first
+        `sinks`."""
+        return _done(_calls.kv_attend_tree(self.handle, self.device, cache._at, cache._dev, q, table, lens, cu_q, max_q,
+                                           max_len, window, sinks, scale, out,
+                                           stream if stream is None else _raw(stream, cache.device), seen),
+                     "mi_decode_kv_attend_tree")
+
+    def kv_keep(self, cache, table, past, keep, cu_keep=None, max_keep=None, *, stream=None):
+        """Of the drafted tokens behind the `past` tokens of each sequence those that are kept move
+        together: keep[cu_keep[b] + i] is the drafted token that becomes the sequence's i-th
+        (int32 [kept tokens]; i at least, or the i-th stays).  Without cu_keep one a sequence;
+        max_keep: the most that a sequence keeps."""
+        _done(_calls.kv_keep(self.handle, self.device, cache._at, cache._dev, table, past, keep, cu_keep, max_keep,
+                             stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_keep")
+
+    def kv_copy(self, cache, src, dst, *, stream=None):
+        """Page dst[i] of the cache becomes a copy of page src[i] (int32 tensors).  Pairs with a page
+        that does not exist are skipped; a page that is written must be in no other pair."""
+        _done(_calls.kv_copy(self.handle, self.device, cache._at, cache._dev, src, dst,
+                             stream if stream is None else _raw(stream, cache.device)), "mi_decode_kv_copy")
+
+    def rms_norm_f8(self, x, weight=None, residual=None, *, eps=1e-6, codes=None, scales=None, total=None, stream=None):
+        """(codes, scales, total) of x [M, K] plus the residual (same shape): total is the sum in
+        x's type (None without a residual), and codes float8_e4m3fn [M, K] times scales float32
+        [M, ceil(K / 128)] are total / sqrt(mean(total^2) + eps) * weight.  Outputs that are given
+        are filled; total may be x or residual."""
+        return _done(_calls.rms_norm_f8(self.handle, self.device, x, weight, residual, eps, codes, scales, total,
+                                        stream if stream is None else _raw(stream, x.device)), "mi_decode_rms_norm_f8")
+
+    def f8_linear(self, x, x_scales, weight, w_scales, *, dtype=torch.float16, bias=None, out=None, stream=None):
+        """x [M, K] with x_scales [M, ceil(K / 128)] times weight [N, K] with w_scales [ceil(N / 128),
+        ceil(K / 128)] (8-bit floats, float32 scales): [M, N] in dtype, sums in float32."""
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+        return _done(_calls.f8_linear(self.handle, self.device, x, x_scales, weight, w_scales, dtype == torch.bfloat16,
+                                      bias, out, stream if stream is None else _raw(stream, x.device)),
+                     "mi_decode_f8_linear")

@@ -51,7 +51,13 @@ constexpr int64_t kJoinInside = 80 << 10;
 constexpr int kItem = 16;   // what starting and ending an item costs, in tiles
 constexpr int kShort = 16;  // tiles of an item that is not worth cutting
 
-template <int CODE, int D, int NT>
+// Keeps the compiler's order of a wave's accesses to its piece of shared memory, as the hardware does.
+__device__ inline void wave_shared() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int CODE, int D, int NT, bool TREE>
 __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kernel(AttendArgs p, int blocks) {
   constexpr int ROWS = 16 * NT, KS = D / 32, DT = D / 16, VW = D / 64;  // VW: 32-bit words of a token's values in a lane
   constexpr int OS = D + 4;
@@ -59,6 +65,9 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
   __shared__ float mbuf[kWaves][ROWS], lbuf[kWaves][ROWS];
   __shared__ u32x4 qbuf[NT > 1 ? NT * KS * 64 : 1];
   __shared__ int last_flag;
+  // of a tree's rows, for each wave: where a window begins, and what they see of the wave's tile
+  __shared__ int from_of[TREE ? kWaves : 1][64];
+  __shared__ uint32_t bits_of[TREE ? kWaves : 1][64];
 
   const int lane = threadIdx.x & 63, tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -69,7 +78,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
   // the line's length, and where this workgroup's piece begins; lane i knows
   // row block `at` + i, and the wave takes its numbers from there
   int at = 0;
-  Block<kTile> mine = block_of<kTile>(p, G, ROWS, blocks, lane, pairs);
+  Block<kTile> mine = block_of<kTile, TREE>(p, G, ROWS, blocks, lane, pairs);
   int64_t total = 0, items = 0;
   int alike = 0;       // not 0: every item has this length on the line
   uint32_t ahead = 0;  // line of the blocks up to the lane's own, for one head
@@ -91,7 +100,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     items += __builtin_popcountll(__ballot(mine.tiles > 0));
     if (at + 64 >= pairs) break;
     at += 64;
-    mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
+    mine = block_of<kTile, TREE>(p, G, ROWS, blocks, at + lane, pairs);
   }
   total *= H, items *= H;
   most = __builtin_amdgcn_readfirstlane(most);
@@ -115,7 +124,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
   if (at > 0) {
     at = 0;
     while (true) {
-      mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
+      mine = block_of<kTile, TREE>(p, G, ROWS, blocks, at + lane, pairs);
       const uint32_t more = extend();
       if ((before + more) * H > begin) break;
       before += more;
@@ -241,6 +250,7 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     h8 qf[NT == 1 ? KS : 1];
     float fac[NT];
     int pos[NT];
+    auto token_of = [&]() { return lane < blk.rows ? (blk.r0 + lane) / G : -1; };  // of the block's row `lane`
     __syncthreads();  // the last item's reads of shared memory are over
     {
       float x[KS][8], top = 0.f;
@@ -279,6 +289,11 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
       if (NT > 1) __syncthreads();
     }
 
+    if (TREE && p.window) {  // read by the lane that writes it
+      const int i = token_of();
+      if (i >= 0) from_of[wave][lane] = tree_row(p, blk.first, i, blk.phi + 1 - blk.start, blk.start, true).from;
+    }
+
     float m[NT], l[NT];
     f32x4 o[NT][DT];
 #pragma unroll
@@ -307,11 +322,22 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
       }
       const bool whole = is_plain && tok0 + kTile - 1 <= blk.plo &&
                          (p.window == 0 || tok0 > blk.phi - p.window || tok0 + kTile - 1 < p.sinks);
-      // whether a query at `at` sees the lane's token c: constants against
+      // whether a row of tile nt sees the lane's token c: constants against
       // numbers of the tile, which otherwise stay in registers as tokens
       const int from = tok0 + 4 * g;
-      auto seen = [&](int c, int at) {
-        const int upto = at - from;
+      // one lane finds a row's bits; kept in registers until they are used, in
+      // its or in every lane, they cost spills (48 rows of 128 channels)
+      if (TREE && !whole) {
+        const int i = token_of();
+        wave_shared();
+        bits_of[wave][lane] = i < 0 ? 0u : tree_bits32(p, {blk.first + i, p.window ? from_of[wave][lane] : 0},
+                                                       blk.phi + 1 - blk.start, blk.start, tok0);
+        wave_shared();
+      }
+      auto sees = [&](int nt) { return TREE ? bits_of[wave][16 * nt + c] >> (4 * g) : 0u; };
+      auto seen = [&](int c, int nt, uint32_t bits) {
+        if constexpr (TREE) return (bits >> c & 1) != 0;
+        const int upto = pos[nt] - from;
         return c <= upto && (p.window == 0 || c > upto - p.window || c < p.sinks - from);
       };
       const int next = tile + kWaves;
@@ -356,11 +382,12 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
           z[nt][1][e] = __builtin_fmaf(z[nt][1][e], f1, log1);
         }
         if (!whole) {
+          const uint32_t bits = sees(nt);
 #pragma unroll
           for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if ((st ? pg1 : pg0) < 0 || !seen(16 * st + e, pos[nt])) z[nt][st][e] = -INFINITY;
+              if ((st ? pg1 : pg0) < 0 || !seen(16 * st + e, nt, bits)) z[nt][st][e] = -INFINITY;
         }
         float top = fmaxf(fmaxf(fmaxf(z[nt][0][0], z[nt][0][1]), fmaxf(z[nt][0][2], z[nt][0][3])),
                           fmaxf(fmaxf(z[nt][1][0], z[nt][1][1]), fmaxf(z[nt][1][2], z[nt][1][3])));
@@ -408,8 +435,10 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
             for (int x = 0; x < VW; ++x)
               if (mine) vraw[e][x] = 0;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              if (mine && seen(16 * (e / 4) + e % 4, pos[nt])) pf[nt][e] = (_Float16)NAN;
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t bits = sees(nt);
+              if (mine && seen(16 * (e / 4) + e % 4, nt, bits)) pf[nt][e] = (_Float16)NAN;
+            }
           }
         }
       }
@@ -512,15 +541,15 @@ __global__ __launch_bounds__(64 * kWaves, NT * D > 384 ? 1 : 2) void attend_kern
     do {
       if (++who == 64) {
         who = 0, at += 64;
-        mine = block_of<kTile>(p, G, ROWS, blocks, at + lane, pairs);
+        mine = block_of<kTile, TREE>(p, G, ROWS, blocks, at + lane, pairs);
       }
       blk = mine.of_lane(who);
     } while (blk.tiles == 0);
   }
 }
 
-template <int CODE, int D, int NT>
-hipError_t run(const AttendArgs& a, hipStream_t s) {
+template <int CODE, int D, int NT, bool TREE>
+hipError_t run_as(const AttendArgs& a, hipStream_t s) {
   constexpr int ROWS = 16 * NT;
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
   const int64_t blocks = (rows + ROWS - 1) / ROWS;
@@ -536,8 +565,15 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   const int64_t part_rows = (by_grid < by_len ? by_grid : by_len) * (rows < ROWS ? rows : ROWS);
   AttendArgs b = a;
   if (part_rows * D * 4 <= kJoinInside) b.join = nullptr;
-  const hipError_t e = launch(attend_kernel<CODE, D, NT>, grid, 64 * kWaves, 0, s, b, (int)blocks);
+  const hipError_t e = launch(attend_kernel<CODE, D, NT, TREE>, grid, 64 * kWaves, 0, s, b, (int)blocks);
   return e != hipSuccess || !b.join ? e : launch_join(b, grid, ROWS, s);
+}
+
+template <int CODE, int D, int NT>
+hipError_t run(const AttendArgs& a, hipStream_t s) {
+  // three tiles of e4m3's 128 channels and a tree's bits spill 80 bytes a lane, four do not
+  constexpr int TREE_NT = CODE == MI_DECODE_E4M3 && D == 128 && NT == 3 ? 4 : NT;
+  return a.seen ? run_as<CODE, D, TREE_NT, true>(a, s) : run_as<CODE, D, NT, false>(a, s);
 }
 
 template <int CODE, int D>

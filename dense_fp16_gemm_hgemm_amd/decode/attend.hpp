@@ -136,7 +136,12 @@ struct Block {
     return k;
   }
 };
-template <int TILE>
+//
+// In a tree every row may see up to the sequence's last token, and `plo` is the
+// last position that the drafts' bits do not speak of: rows stand at plo + 1 at
+// least, which moves a window's border by one in what is loaded, and what is
+// seen of that goes by each row's own position.
+template <int TILE, bool TREE>
 __device__ inline Block<TILE> block_of(const AttendArgs& p, int G, int block_rows, int blocks, int pair, int pairs) {
   Block<TILE> k = {};
   if (pair >= pairs) return k;
@@ -153,6 +158,7 @@ __device__ inline Block<TILE> block_of(const AttendArgs& p, int G, int block_row
   k.start = len - sp.n;
   k.plo = k.start + k.r0 / G;
   k.phi = k.start + (k.r0 + k.rows - 1) / G;
+  if (TREE) k.plo = k.start - 1, k.phi = len - 1;
   if (p.window) {
     const int lo = max(0, k.plo - p.window + 1);
     k.lo = lo / TILE;
@@ -160,6 +166,49 @@ __device__ inline Block<TILE> block_of(const AttendArgs& p, int G, int block_row
   }
   k.tiles = k.rows <= 0 ? 0 : max(1, k.ns + max(k.phi, 0) / TILE + 1 - k.lo);
   return k;
+}
+
+// A row of a tree: its token of the call, and with a window the first position
+// of the context that is in it.
+struct TreeRow {
+  int token;  // -1: there is no row
+  int from;
+};
+__device__ inline uint32_t seen_word(const AttendArgs& p, int token, int w) {
+  return w < p.seen_words ? (uint32_t)p.seen[token * p.seen_stride + w] : 0u;
+}
+// Token `i` of the n drafted ones, which lie from position start on and begin with token `first` of the call.
+__device__ inline TreeRow tree_row(const AttendArgs& p, int first, int i, int n, int start, bool in) {
+  TreeRow t = {in ? first + i : -1, 0};
+  if (p.window && in) {
+    int others = 0;
+    for (int w = 0; 32 * w < n; ++w) {
+      uint32_t x = seen_word(p, t.token, w);
+      if (n - 32 * w < 32) x &= (1u << (n - 32 * w)) - 1;
+      if (i / 32 == w) x &= ~(1u << (i % 32));
+      others += __builtin_popcount(x);
+    }
+    t.from = start + others - p.window + 1;
+  }
+  return t;
+}
+// Which of the positions at .. at + 31 a row sees, as bits.
+__device__ inline uint32_t tree_bits32(const AttendArgs& p, const TreeRow& t, int n, int start, int at) {
+  auto ones = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+  if (t.token < 0) return 0;
+  const int off = at - start;
+  uint32_t drafts = 0;
+  if (off > -32 && off < n) {
+    const uint32_t lo = seen_word(p, t.token, max(off, 0) / 32), hi = seen_word(p, t.token, off / 32 + 1);
+    drafts = (off < 0 ? lo << -off : __builtin_amdgcn_alignbit(hi, lo, off % 32)) & ones(n - off);
+  }
+  uint32_t context = ones(-off);
+  if (p.window) context &= ~ones(t.from - at) | ones(p.sinks - at);
+  return context | drafts;
+}
+// At .. at + 63.
+__device__ inline uint64_t tree_bits64(const AttendArgs& p, const TreeRow& t, int n, int start, int at) {
+  return tree_bits32(p, t, n, start, at) | (uint64_t)tree_bits32(p, t, n, start, at + 32) << 32;
 }
 
 // Four channels of a row's result: row r of the sequence whose first token is

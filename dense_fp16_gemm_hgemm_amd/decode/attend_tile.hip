@@ -58,7 +58,7 @@ __device__ inline void schedule_reads() {
   __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
 }
 
-template <int CODE, int D, int NW>
+template <int CODE, int D, int NW, bool TREE>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs p, int blocks, int splits) {
   constexpr int ROWS = 32 * NW, KS = D / 16, DT = D / 32, T = 64 * NW;
   constexpr int UNITS = kStage * D / 16, UN = (UNITS + T - 1) / T;  // 16-byte units of a stage, and a thread's
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   // most, come first.
   const int heads = p.batch.batch * H, bh = blockIdx.x % heads, rest = blockIdx.x / heads;
   const int j = rest % splits, rb = blocks - 1 - rest / splits, h = bh % H;
-  const Block<kStage> blk = block_of<kStage>(p, G, ROWS, blocks, bh / H * blocks + rb, p.batch.batch * blocks);
+  const Block<kStage> blk = block_of<kStage, TREE>(p, G, ROWS, blocks, bh / H * blocks + rb, p.batch.batch * blocks);
   const int parts = blk.tiles == 0 ? 0 : min(splits, max(1, blk.tiles / 4)), item = rb * heads + bh;
   if (splits > 1 && j == 0 && tid == 0) {
     const uint32_t at = (uint32_t)(item * splits) * kPart;
@@ -199,6 +199,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   const int row = 32 * wave + col;
   const bool in = row < blk.rows;
   const int pos = in ? blk.start + (blk.r0 + row) / G : -1;
+  TreeRow tree;
+  if constexpr (TREE) tree = tree_row(p, blk.first, (blk.r0 + row) / G, blk.phi + 1 - blk.start, blk.start, in);
   entries(s0);
   u32x4 qraw[KS];
   {
@@ -254,7 +256,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
 
   // rows of the wave that exist, and their positions
   const int wrows = min(32, blk.rows - 32 * wave);
-  const int wlo = blk.start + (blk.r0 + 32 * wave) / G, whi = blk.start + (blk.r0 + 32 * wave + wrows - 1) / G;
+  const int wlo = TREE ? blk.plo : blk.start + (blk.r0 + 32 * wave) / G;
+  const int whi = TREE ? blk.phi : blk.start + (blk.r0 + 32 * wave + wrows - 1) / G;
   // pieces of the operands: the key's of token `col`, the value's of channel `col`
   // for four of them; the others are whole steps away
   int kx[4], vx[4];
@@ -291,11 +294,16 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     // Token c after the lane's first one (constants, compared with numbers of
     // the stage: left as tokens, 32 of them would stay in registers).
     const int upto = pos - t0 - 4 * hi, after = p.window ? upto - p.window : -1, sink = p.sinks - t0 - 4 * hi;
-    auto seen = [&](int c) { return c <= upto && (c > after || c < sink); };
+    uint64_t sees = 0;
+    auto seen = [&](int c) {
+      if constexpr (TREE) return (sees >> c & 1) != 0;
+      return c <= upto && (c > after || c < sink);
+    };
     const int valid = __ballot(mine.page >= 0) & 15;
     const bool plain = vs.rest == 1.f && mine.ks >= 0.f && mine.ks < INFINITY;
     const bool whole = valid == 15 && __all(plain) && t0 + kStage - 1 <= wlo &&
                        (p.window == 0 || t0 > whi - p.window || t0 + kStage - 1 < p.sinks);
+    if (TREE && !(whole && (CODE == MI_DECODE_INT8 || nans[n3] == 0))) sees = tree_bits64(p, tree, blk.phi + 1 - blk.start, blk.start, t0) >> (4 * hi);
     float f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = fac * lane_value(mine.ks, i);
@@ -426,8 +434,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   }
 }
 
-template <int CODE, int D, int NW>
-hipError_t run(const AttendArgs& a, hipStream_t s) {
+template <int CODE, int D, int NW, bool TREE>
+hipError_t run_as(const AttendArgs& a, hipStream_t s) {
   constexpr int ROWS = 32 * NW;
   const int64_t rows = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.max_tokens;
   const int64_t blocks = (rows + ROWS - 1) / ROWS;
@@ -439,8 +447,13 @@ hipError_t run(const AttendArgs& a, hipStream_t s) {
   if (splits > stages / 4) splits = stages / 4 > 0 ? stages / 4 : 1;
   if (items * splits * part_bytes(ROWS, D) > MI_DECODE_WORKSPACE_BYTES) splits = 1;
   const hipError_t e =
-      launch(attend_tile_kernel<CODE, D, NW>, (unsigned)(items * splits), 64 * NW, 0, s, a, (int)blocks, (int)splits);
+      launch(attend_tile_kernel<CODE, D, NW, TREE>, (unsigned)(items * splits), 64 * NW, 0, s, a, (int)blocks, (int)splits);
   return e != hipSuccess || splits == 1 ? e : launch_join(a, (int)items, ROWS, s);
+}
+
+template <int CODE, int D, int NW>
+hipError_t run(const AttendArgs& a, hipStream_t s) {
+  return a.seen ? run_as<CODE, D, NW, true>(a, s) : run_as<CODE, D, NW, false>(a, s);
 }
 
 // 256 channels: a row's sums, queries and logits need more registers than two

@@ -24,6 +24,8 @@ struct DeviceGuard {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool is16(int dtype) { return dtype == MI_DECODE_F16 || dtype == MI_DECODE_BF16; }
 
+constexpr int64_t kFar = int64_t(1) << 30;  // rows' distances: 2^31 of them stay within 64 bits
+
 struct Extent {
   uintptr_t lo, hi;  // bytes [lo, hi)
 };
@@ -118,6 +120,56 @@ mi_decode_status_t check_rows(const mi_decode_rows_t* r, int64_t heads, int64_t 
     const mi_decode_status_t st_ = (x);              \
     if (st_ != MI_DECODE_OK) return st_;             \
   } while (0)
+
+// Both forms of attention; seen is nullptr for the one in order.
+static mi_decode_status_t attend(mi_decode_handle_t h, const mi_decode_cache_t* cache, mi_decode_dtype_t dtype,
+                                 const mi_decode_batch_t* batch, int64_t max_len, int32_t q_heads,
+                                 const mi_decode_rows_t* q, const mi_decode_rows_t* out, const int32_t* seen,
+                                 int64_t seen_stride, int32_t seen_words, float scale, int32_t window,
+                                 int32_t sinks, void* stream) {
+  if (!h) return MI_DECODE_ERR_INVALID_ARG;
+  TRY(check_cache(cache));
+  TRY(check_batch(cache, batch));
+  if (!is16(dtype)) return MI_DECODE_ERR_UNSUPPORTED;
+  if (max_len < 0 || q_heads < 1 || window < 0 || sinks < 0 || !(scale == scale) || scale - scale != 0.f)
+    return MI_DECODE_ERR_INVALID_ARG;
+  if (q_heads % cache->kv_heads) return MI_DECODE_ERR_INVALID_ARG;
+  if ((int64_t)q_heads / cache->kv_heads * (batch->max_tokens > 0 ? batch->max_tokens : 1) > (1 << 24))
+    return MI_DECODE_ERR_UNSUPPORTED;
+  if (batch->batch == 0 || batch->tokens == 0) return MI_DECODE_OK;
+  // a sequence's heads on the line of work are counted in 32 bits
+  if (((int64_t)batch->table_cols * cache->page_size / 32 + 32) * cache->kv_heads > INT32_MAX)
+    return MI_DECODE_ERR_UNSUPPORTED;
+  TRY(check_rows(q, q_heads, cache->head_dim));
+  TRY(check_rows(out, q_heads, cache->head_dim));
+  if (batch->tokens > 1 && out->token_stride < cache->head_dim) return MI_DECODE_ERR_INVALID_ARG;
+  if (overlap(extent(*out, batch->tokens, q_heads, cache->head_dim),
+              extent(*q, batch->tokens, q_heads, cache->head_dim)))
+    return MI_DECODE_ERR_INVALID_ARG;
+  if (h->no_device) return MI_DECODE_ERR_NO_DEVICE;
+  AttendArgs a = {};
+  a.cache = *cache;
+  a.batch = *batch;
+  a.bf16 = dtype == MI_DECODE_BF16;
+  a.q = *q;
+  a.out = *out;
+  a.max_len = max_len;
+  a.q_heads = q_heads;
+  // positions are below 2^30: a longer window hides nothing, and the kernels'
+  // differences of positions and these stay within 32 bits
+  a.window = window < (1 << 30) ? window : 0;
+  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
+  a.scale = scale;
+  a.seen = seen;
+  a.seen_stride = seen_stride;
+  a.seen_words = seen_words;
+  a.ws = h->ws;
+  a.cnt = h->cnt;
+  a.join = reinterpret_cast<JoinItem*>(h->cnt + kCounters);
+  a.cus = h->cus;
+  DeviceGuard g(h->device);
+  return done(h, launch_attend(a, (hipStream_t)stream));
+}
 
 extern "C" {
 
@@ -236,6 +288,17 @@ mi_decode_status_t mi_decode_kv_append(mi_decode_handle_t h, const mi_decode_cac
                                        int32_t interleaved, int32_t q_heads,
                                        const mi_decode_rows_t* q, const mi_decode_rows_t* q_out,
                                        void* stream) {
+  return mi_decode_kv_append_at(h, cache, dtype, batch, k, v, rope, rope_rows, rot_dim, interleaved,
+                                nullptr, q_heads, q, q_out, stream);
+}
+
+mi_decode_status_t mi_decode_kv_append_at(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                          mi_decode_dtype_t dtype, const mi_decode_batch_t* batch,
+                                          const mi_decode_rows_t* k, const mi_decode_rows_t* v,
+                                          const float* rope, int64_t rope_rows, int32_t rot_dim,
+                                          int32_t interleaved, const int32_t* positions,
+                                          int32_t q_heads, const mi_decode_rows_t* q,
+                                          const mi_decode_rows_t* q_out, void* stream) {
   if (!h) return MI_DECODE_ERR_INVALID_ARG;
   TRY(check_cache(cache));
   TRY(check_batch(cache, batch));
@@ -243,8 +306,9 @@ mi_decode_status_t mi_decode_kv_append(mi_decode_handle_t h, const mi_decode_cac
   if (q_heads < 0 || rope_rows < 0 || rot_dim < 0) return MI_DECODE_ERR_INVALID_ARG;
   const int32_t D = cache->head_dim;
   if (rope) {
-    if (rot_dim > D || rope_rows < (int64_t)batch->table_cols * cache->page_size || rope_rows < 1)
-      return MI_DECODE_ERR_INVALID_ARG;
+    const int64_t least = positions ? 1 : (int64_t)batch->table_cols * cache->page_size;
+    if (rot_dim > D || rope_rows < least || rope_rows < 1) return MI_DECODE_ERR_INVALID_ARG;
+    if (!aligned(positions, 4)) return MI_DECODE_ERR_UNSUPPORTED;
     if (rot_dim % 16 || rot_dim == 0 || !aligned(rope, 16)) return MI_DECODE_ERR_UNSUPPORTED;
   }
   if (batch->batch == 0 || batch->tokens == 0) return MI_DECODE_OK;
@@ -277,6 +341,7 @@ mi_decode_status_t mi_decode_kv_append(mi_decode_handle_t h, const mi_decode_cac
   a.v = *v;
   a.rope = rope;
   a.rope_rows = rope_rows;
+  a.positions = positions;
   a.rot_dim = rope ? rot_dim : 0;
   a.interleaved = interleaved != 0;
   DeviceGuard g(h->device);
@@ -309,45 +374,148 @@ mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cac
                                        int64_t max_len, int32_t q_heads, const mi_decode_rows_t* q,
                                        const mi_decode_rows_t* out, float scale, int32_t window,
                                        int32_t sinks, void* stream) {
+  return attend(h, cache, dtype, batch, max_len, q_heads, q, out, nullptr, 0, 0, scale, window, sinks, stream);
+}
+
+mi_decode_status_t mi_decode_kv_attend_tree(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                            mi_decode_dtype_t dtype, const mi_decode_batch_t* batch,
+                                            int64_t max_len, int32_t q_heads,
+                                            const mi_decode_rows_t* q, const mi_decode_rows_t* out,
+                                            const int32_t* seen, int64_t seen_stride,
+                                            int32_t seen_words, float scale, int32_t window,
+                                            int32_t sinks, void* stream) {
+  if (!h || !batch || seen_words < 0 || seen_stride < seen_words) return MI_DECODE_ERR_INVALID_ARG;
+  if (batch->batch > 0 && batch->tokens > 0) {
+    if (!seen || (int64_t)seen_words * 32 < batch->max_tokens) return MI_DECODE_ERR_INVALID_ARG;
+    if (!aligned(seen, 4)) return MI_DECODE_ERR_UNSUPPORTED;
+  }
+  return attend(h, cache, dtype, batch, max_len, q_heads, q, out, seen, seen_stride, seen_words, scale, window,
+                sinks, stream);
+}
+
+mi_decode_status_t mi_decode_kv_keep(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                     const mi_decode_batch_t* batch, const int32_t* keep,
+                                     void* stream) {
   if (!h) return MI_DECODE_ERR_INVALID_ARG;
   TRY(check_cache(cache));
   TRY(check_batch(cache, batch));
-  if (!is16(dtype)) return MI_DECODE_ERR_UNSUPPORTED;
-  if (max_len < 0 || q_heads < 1 || window < 0 || sinks < 0 || !(scale == scale) || scale - scale != 0.f)
-    return MI_DECODE_ERR_INVALID_ARG;
-  if (q_heads % cache->kv_heads) return MI_DECODE_ERR_INVALID_ARG;
-  if ((int64_t)q_heads / cache->kv_heads * (batch->max_tokens > 0 ? batch->max_tokens : 1) > (1 << 24))
-    return MI_DECODE_ERR_UNSUPPORTED;
   if (batch->batch == 0 || batch->tokens == 0) return MI_DECODE_OK;
-  // a sequence's heads on the line of work are counted in 32 bits
-  if (((int64_t)batch->table_cols * cache->page_size / 32 + 32) * cache->kv_heads > INT32_MAX)
-    return MI_DECODE_ERR_UNSUPPORTED;
-  TRY(check_rows(q, q_heads, cache->head_dim));
-  TRY(check_rows(out, q_heads, cache->head_dim));
-  if (batch->tokens > 1 && out->token_stride < cache->head_dim) return MI_DECODE_ERR_INVALID_ARG;
-  if (overlap(extent(*out, batch->tokens, q_heads, cache->head_dim),
-              extent(*q, batch->tokens, q_heads, cache->head_dim)))
-    return MI_DECODE_ERR_INVALID_ARG;
+  if (!keep) return MI_DECODE_ERR_INVALID_ARG;
+  if (!aligned(keep, 4)) return MI_DECODE_ERR_UNSUPPORTED;
   if (h->no_device) return MI_DECODE_ERR_NO_DEVICE;
-  AttendArgs a = {};
+  KeepArgs a = {};
   a.cache = *cache;
   a.batch = *batch;
-  a.bf16 = dtype == MI_DECODE_BF16;
-  a.q = *q;
-  a.out = *out;
-  a.max_len = max_len;
-  a.q_heads = q_heads;
-  // positions are below 2^30: a longer window hides nothing, and the kernels'
-  // differences of positions and these stay within 32 bits
-  a.window = window < (1 << 30) ? window : 0;
-  a.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
-  a.scale = scale;
-  a.ws = h->ws;
-  a.cnt = h->cnt;
-  a.join = reinterpret_cast<JoinItem*>(h->cnt + kCounters);
-  a.cus = h->cus;
+  a.keep = keep;
   DeviceGuard g(h->device);
-  return done(h, launch_attend(a, (hipStream_t)stream));
+  return done(h, launch_keep(a, (hipStream_t)stream));
+}
+
+mi_decode_status_t mi_decode_kv_copy(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                     const int32_t* src, const int32_t* dst, int64_t pairs,
+                                     void* stream) {
+  if (!h || pairs < 0) return MI_DECODE_ERR_INVALID_ARG;
+  TRY(check_cache(cache));
+  if (pairs == 0 || cache->pages == 0) return MI_DECODE_OK;
+  if (!src || !dst) return MI_DECODE_ERR_INVALID_ARG;
+  if (!aligned(src, 4) || !aligned(dst, 4)) return MI_DECODE_ERR_UNSUPPORTED;
+  if (h->no_device) return MI_DECODE_ERR_NO_DEVICE;
+  CopyArgs a = {*cache, src, dst, pairs};
+  DeviceGuard g(h->device);
+  return done(h, launch_copy(a, (hipStream_t)stream));
+}
+
+mi_decode_status_t mi_decode_rms_norm_f8(mi_decode_handle_t h, mi_decode_dtype_t dtype, int64_t M,
+                                         int64_t K, const void* x, int64_t ldx,
+                                         const void* residual, int64_t ldr, const void* weight,
+                                         float eps, void* codes, int64_t ldc, float* scales,
+                                         int64_t lds, void* total, int64_t ldt, void* stream) {
+  if (!h || M < 0 || K < 0 || !(eps >= 0.f) || eps - eps != 0.f) return MI_DECODE_ERR_INVALID_ARG;
+  if (!is16(dtype) || M > INT32_MAX || K > (1 << 30)) return MI_DECODE_ERR_UNSUPPORTED;
+  for (const int64_t ld : {ldx, ldr, ldc, lds, ldt})
+    if (ld > kFar) return MI_DECODE_ERR_UNSUPPORTED;
+  if (M == 0 || K == 0) return MI_DECODE_OK;
+  const int64_t blocks = (K + 127) / 128;
+  if (!x || !codes || !scales || (total && !residual)) return MI_DECODE_ERR_INVALID_ARG;
+  if (M > 1 && (ldx < K || ldc < K || lds < blocks || (residual && ldr < K) || (total && ldt < K)))
+    return MI_DECODE_ERR_INVALID_ARG;
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(weight, 2) || !aligned(total, 2) || !aligned(scales, 4))
+    return MI_DECODE_ERR_UNSUPPORTED;
+  auto rows = [&](const void* p, int64_t ld, int64_t n, int64_t size) { return extent(p, size * ((M - 1) * ld + n)); };
+  const Extent in[3] = {rows(x, ldx, K, 2), rows(residual, ldr, K, 2), extent(weight, 2 * K)};
+  const Extent out[3] = {rows(codes, ldc, K, 1), rows(scales, lds, blocks, 4), rows(total, ldt, K, 2)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return MI_DECODE_ERR_INVALID_ARG;
+    for (int j = 0; j < 3; ++j) {
+      // a row is read before its total is written, element by element
+      const bool same = i == 2 && ((j == 0 && total == x && (M == 1 || ldt == ldx)) ||
+                                   (j == 1 && total == residual && (M == 1 || ldt == ldr)));
+      if (!same && overlap(out[i], in[j])) return MI_DECODE_ERR_INVALID_ARG;
+    }
+  }
+  if (h->no_device) return MI_DECODE_ERR_NO_DEVICE;
+  NormArgs a = {};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.total = total;
+  a.ldx = M > 1 ? ldx : 0;
+  a.ldr = M > 1 ? ldr : 0;
+  a.ldc = M > 1 ? ldc : 0;
+  a.lds = M > 1 ? lds : 0;
+  a.ldt = M > 1 ? ldt : 0;
+  a.M = M;
+  a.K = (int32_t)K;
+  a.eps = eps;
+  a.bf16 = dtype == MI_DECODE_BF16;
+  DeviceGuard g(h->device);
+  return done(h, launch_norm(a, (hipStream_t)stream));
+}
+
+mi_decode_status_t mi_decode_f8_linear(mi_decode_handle_t h, mi_decode_dtype_t dtype, int64_t M,
+                                       int64_t N, int64_t K, const void* x, int64_t ldx,
+                                       const float* xs, int64_t ldxs, const void* w, int64_t ldw,
+                                       const float* ws, int64_t ldws, const void* bias, void* y,
+                                       int64_t ldy, void* stream) {
+  if (!h || M < 0 || N < 0 || K < 0) return MI_DECODE_ERR_INVALID_ARG;
+  // row numbers of whole tiles fit in 32 bits
+  if (!is16(dtype) || M > INT32_MAX - 255 || N > INT32_MAX - 255 || K > (1 << 30)) return MI_DECODE_ERR_UNSUPPORTED;
+  for (const int64_t ld : {ldx, ldxs, ldw, ldws, ldy})
+    if (ld > kFar) return MI_DECODE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return MI_DECODE_OK;
+  const int64_t kb = (K + 127) / 128, nb = (N + 127) / 128;
+  if (!y || (K > 0 && (!x || !xs || !w || !ws))) return MI_DECODE_ERR_INVALID_ARG;
+  if ((M > 1 && (ldx < K || ldxs < kb || ldy < N)) || (N > 1 && ldw < K) || (nb > 1 && ldws < kb))
+    return MI_DECODE_ERR_INVALID_ARG;
+  if (!aligned(xs, 4) || !aligned(ws, 4) || !aligned(bias, 2) || !aligned(y, 2)) return MI_DECODE_ERR_UNSUPPORTED;
+  const Extent ey = extent(y, 2 * ((M - 1) * ldy + N));
+  if (K > 0 && (overlap(ey, extent(x, (M - 1) * ldx + K)) || overlap(ey, extent(w, (N - 1) * ldw + K)) ||
+                overlap(ey, extent(xs, 4 * ((M - 1) * ldxs + kb))) || overlap(ey, extent(ws, 4 * ((nb - 1) * ldws + kb)))))
+    return MI_DECODE_ERR_INVALID_ARG;
+  if (overlap(ey, extent(bias, 2 * N))) return MI_DECODE_ERR_INVALID_ARG;
+  if (h->no_device) return MI_DECODE_ERR_NO_DEVICE;
+  F8Args a = {};
+  a.x = static_cast<const uint8_t*>(x);
+  a.w = static_cast<const uint8_t*>(w);
+  a.xs = xs;
+  a.ws = ws;
+  a.bias = bias;
+  a.y = y;
+  a.ldx = M > 1 ? ldx : 0;
+  a.ldxs = M > 1 ? ldxs : 0;
+  a.ldw = N > 1 ? ldw : 0;
+  a.ldws = nb > 1 ? ldws : 0;
+  a.ldy = M > 1 ? ldy : 0;
+  a.M = (int32_t)M;
+  a.N = (int32_t)N;
+  a.K = (int32_t)K;
+  a.cus = h->cus;
+  a.bf16 = dtype == MI_DECODE_BF16;
+  DeviceGuard g(h->device);
+  return done(h, launch_f8(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

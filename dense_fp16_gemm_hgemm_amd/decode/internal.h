@@ -31,6 +31,7 @@ struct AppendArgs : KvArgs {
   mi_decode_rows_t k, v, q, q_out;
   const float* rope;  // nullptr: no rotation
   int64_t rope_rows;
+  const int32_t* positions;  // [tokens] rows of rope, nullptr: those of the tokens' places
   int32_t rot_dim, interleaved, q_heads;
 };
 
@@ -55,6 +56,46 @@ struct AttendArgs : KvArgs {
   int* cnt;   // arrival counters, zero between launches
   JoinItem* join;  // what a second kernel joins, or nullptr: the last workgroup does
   int cus;    // the device's compute units
+  const int32_t* seen;  // drafted tokens that a token sees, nullptr: it sees all up to itself
+  int64_t seen_stride;
+  int32_t seen_words;
+};
+
+struct KeepArgs : KvArgs {
+  const int32_t* keep;
+};
+
+struct CopyArgs {
+  mi_decode_cache_t cache;
+  const int32_t* src;
+  const int32_t* dst;
+  int64_t pairs;
+};
+
+struct NormArgs {
+  const void* x;
+  const void* residual;  // nullptr: none
+  const void* weight;    // nullptr: 1
+  uint8_t* codes;
+  float* scales;
+  void* total;  // nullptr: not wanted
+  int64_t ldx, ldr, ldc, lds, ldt, M;
+  int32_t K;
+  float eps;
+  int32_t bf16;
+};
+
+struct F8Args {
+  const uint8_t* x;
+  const uint8_t* w;
+  const float* xs;
+  const float* ws;
+  const void* bias;  // nullptr: none
+  void* y;
+  int64_t ldx, ldxs, ldw, ldws, ldy;
+  int32_t M, N, K;
+  int32_t cus;  // the device's compute units
+  int32_t bf16;
 };
 
 // Enqueues a kernel and returns its own launch's status: the runtime's last error
@@ -73,6 +114,10 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 hipError_t launch_read(const ReadArgs& a, hipStream_t s);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s);       // any number of rows
 hipError_t launch_attend_tile(const AttendArgs& a, hipStream_t s);  // many rows a sequence
+hipError_t launch_keep(const KeepArgs& a, hipStream_t s);
+hipError_t launch_copy(const CopyArgs& a, hipStream_t s);
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_f8(const F8Args& a, hipStream_t s);
 
 // Adds the parts of `items` listed blocks of at most block_rows rows.
 hipError_t launch_join(const AttendArgs& a, int items, int block_rows, hipStream_t s);

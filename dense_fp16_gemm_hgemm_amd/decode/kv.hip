@@ -61,7 +61,7 @@ struct Angles {
 };
 __device__ __forceinline__ Angles load_angles(const AppendArgs& p, int c, int64_t pos) {
   Angles g;
-  const float* row = p.rope + min(pos, p.rope_rows - 1) * p.rot_dim + 8 * c;
+  const float* row = p.rope + max(min(pos, p.rope_rows - 1), (int64_t)0) * p.rot_dim + 8 * c;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const f32x4 u = *reinterpret_cast<const f32x4*>(row + 4 * i);
@@ -70,6 +70,10 @@ __device__ __forceinline__ Angles load_angles(const AppendArgs& p, int c, int64_
     for (int e = 0; e < 4; ++e) g.co[4 * i + e] = u[e], g.si[4 * i + e] = w[e];
   }
   return g;
+}
+// The row of rope for token t of the call, which comes to position pos.
+__device__ __forceinline__ int64_t rope_row(const AppendArgs& p, int64_t t, int64_t pos) {
+  return p.positions ? p.positions[t] : pos;
 }
 __device__ __forceinline__ void turn(Chunk& x, const Angles& g, bool interleaved) {
   if (!interleaved) {
@@ -92,14 +96,14 @@ __device__ __forceinline__ void turn(Chunk& x, const Angles& g, bool interleaved
   }
 }
 
-// A chunk of a new key (turned) or value row.
+// A chunk of a new key (turned) or value row: token t of the call, for position pos.
 template <bool BF16>
-__device__ __forceinline__ Chunk load_chunk(const AppendArgs& p, const uint16_t* row, int c, int64_t pos, bool rotate) {
+__device__ __forceinline__ Chunk load_chunk(const AppendArgs& p, const uint16_t* row, int c, int64_t t, int64_t pos, bool rotate) {
   Chunk x;
   const Place at = place_of(c, rotate ? p.rot_dim : 0, p.interleaved);
   load8<BF16>(x.a, row + at.a);
   load8<BF16>(x.b, row + at.b);
-  if (at.turns) turn(x, load_angles(p, c, pos), p.interleaved);
+  if (at.turns) turn(x, load_angles(p, c, rope_row(p, t, pos)), p.interleaved);
   return x;
 }
 
@@ -212,7 +216,7 @@ __device__ __forceinline__ void append_page(const AppendArgs& p, int line, int h
   const int n = (int)(hi - lo);
   const int64_t t0 = sp.first + (lo - past);
   const float old = fill ? *scale : 0.f;
-  auto fetch = [&](int r) { return load_chunk<BF16>(p, base + (t0 + r) * token_stride, c, lo + r, is_k); };
+  auto fetch = [&](int r) { return load_chunk<BF16>(p, base + (t0 + r) * token_stride, c, t0 + r, lo + r, is_k); };
   uint32_t m = 0;
   auto widen = [&](const Chunk& x) {
 #pragma unroll
@@ -292,7 +296,7 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& p, int64_t item) 
   const uint16_t* row = static_cast<const uint16_t*>(p.q.data) + t * p.q.token_stride;
   uint16_t* to = static_cast<uint16_t*>(p.q_out.data) + t * p.q_out.token_stride;
   Angles g;
-  if (at.turns) g = load_angles(p, c, pos);
+  if (at.turns) g = load_angles(p, c, rope_row(p, t, pos));
   Chunk x[HEADS];
 #pragma unroll
   for (int k = 0; k < HEADS; ++k)

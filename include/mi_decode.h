@@ -8,7 +8,15 @@
  *   mi_decode_kv_append  keys and values of new tokens into a paged 8-bit
  *                        cache, rotated by their positions on the way;
  *   mi_decode_kv_read    the values of a range of cached tokens;
- *   mi_decode_kv_attend  attention over that cache.
+ *   mi_decode_kv_attend  attention over that cache;
+ *   mi_decode_rms_norm_f8     norm, with the residual's addition, into 8-bit
+ *                             floats with a scale for 128 columns;
+ *   mi_decode_f8_linear       linear layer of 8-bit floats with block scales,
+ *                             for any number of tokens;
+ *   mi_decode_kv_append_at    append with positions of its own for the rotation;
+ *   mi_decode_kv_attend_tree  attention for a tree of drafted tokens;
+ *   mi_decode_kv_keep         the drafted tokens that are kept move together;
+ *   mi_decode_kv_copy         copies of pages.
  *
  * Conventions for every function:
  *   - Pointers are DEVICE pointers on the handle's device (the cache descriptor
@@ -20,9 +28,10 @@
  *     be captured into a graph.
  *   - No exception crosses the ABI; every failure is a status code, and no work
  *     is enqueued then.
- *   - mi_decode_kv_attend keeps partial results in the handle's workspace:
- *     launches of one handle that may run at the same time on different
- *     streams must use separate handles.  The other operators use no workspace.
+ *   - mi_decode_kv_attend and mi_decode_kv_attend_tree keep partial results in
+ *     the handle's workspace: launches of one handle that may run at the same
+ *     time on different streams must use separate handles.  The other operators
+ *     use no workspace.
  *   - Page tables, lengths and offsets are read by the kernels.  A page number
  *     outside 0 .. pages-1 is never followed: tokens on it are skipped (not
  *     appended, read as zeros, not attended to).  Lengths and offsets are
@@ -57,7 +66,7 @@ typedef enum { MI_DECODE_INT8 = 0, MI_DECODE_E4M3 = 1 } mi_decode_code_t;
 #define MI_DECODE_CREATE_NO_DEVICE 1u /* inspection handle: arguments are checked, nothing launches */
 
 /* Create a handle on the current HIP device.  Allocates the workspace of
- * mi_decode_kv_attend once (MI_DECODE_WORKSPACE_BYTES).  Returns OK,
+ * mi_decode_kv_attend and mi_decode_kv_attend_tree once (MI_DECODE_WORKSPACE_BYTES).  Returns OK,
  * INVALID_ARG (out NULL), NO_DEVICE or ERR_HIP (no memory). */
 #define MI_DECODE_WORKSPACE_BYTES (64u << 20)
 mi_decode_status_t mi_decode_create(mi_decode_handle_t* out, uint32_t flags);
@@ -205,6 +214,122 @@ mi_decode_status_t mi_decode_kv_attend(mi_decode_handle_t h, const mi_decode_cac
                                        int64_t max_len, int32_t q_heads, const mi_decode_rows_t* q,
                                        const mi_decode_rows_t* out, float scale, int32_t window,
                                        int32_t sinks, void* stream);
+
+/*
+ * As mi_decode_kv_append, but token t of the call is turned by row
+ * positions[t] of the rope table (int32 [tokens], clamped to 0 .. rope_rows - 1),
+ * and so is its query; it still takes the place lens[b] + i in the cache.
+ * Drafted tokens of a tree have the positions of their depths so, wherever they
+ * lie.  rope_rows need not cover the table's positions.  positions NULL: as
+ * mi_decode_kv_append.
+ */
+mi_decode_status_t mi_decode_kv_append_at(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                          mi_decode_dtype_t dtype, const mi_decode_batch_t* batch,
+                                          const mi_decode_rows_t* k, const mi_decode_rows_t* v,
+                                          const float* rope, int64_t rope_rows, int32_t rot_dim,
+                                          int32_t interleaved, const int32_t* positions,
+                                          int32_t q_heads, const mi_decode_rows_t* q,
+                                          const mi_decode_rows_t* q_out, void* stream);
+
+/*
+ * Attention for drafted tokens, several continuations of a sequence at once.
+ * As in mi_decode_kv_attend sequence b's n query tokens are the last n of its
+ * lens[b] tokens in the cache; the c = lens[b] - n tokens before them are its
+ * context.  Bit a % 32 of word a / 32 of row t of `seen` (int32
+ * [tokens][seen_words], rows seen_stride apart) says whether token t of the
+ * call sees its sequence's drafted token a, which may be itself; bits from n on
+ * say nothing.  For a tree these are a token's ancestors and itself.  Token t sees
+ *   - context position j < c where window == 0, or j > p - window, or j < sinks,
+ *     with p = c + the number of drafted tokens other than itself that it sees
+ *     (for a tree, the position of its depth);
+ *   - drafted tokens by their bits alone, whatever the window is.
+ * seen_words * 32 must be at least batch->max_tokens, and seen_stride at least
+ * seen_words.  A query that sees nothing gives zeros.  Everything else is as in
+ * mi_decode_kv_attend.
+ */
+mi_decode_status_t mi_decode_kv_attend_tree(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                            mi_decode_dtype_t dtype, const mi_decode_batch_t* batch,
+                                            int64_t max_len, int32_t q_heads,
+                                            const mi_decode_rows_t* q, const mi_decode_rows_t* out,
+                                            const int32_t* seen, int64_t seen_stride,
+                                            int32_t seen_words, float scale, int32_t window,
+                                            int32_t sinks, void* stream);
+
+/*
+ * The drafted tokens that are kept move to the front of the drafts: token i of
+ * sequence b, i < cu[b + 1] - cu[b], comes to position lens[b] + i from position
+ * lens[b] + keep[cu[b] + i], where lens holds the tokens before the drafts.
+ * All are as if they moved at once.  An entry with keep < i (so a negative
+ * one), or whose source has no valid page, leaves its position as it is; a
+ * position without a valid page is skipped.  Indices need not ascend, and one
+ * may be there more than once.
+ * Scales.  For each page and head that positions lens[b] .. lens[b] + n - 1 lie
+ * on: s' = max(s, max |x| / QMAX) over the tokens x that come from other pages.
+ * Codes become round(code * (s_source / s')), 0 where s' is 0, with s' and the
+ * ratio in binary64: those that come, and, where s' > s, those of all positions
+ * up to lens[b] + n - 1 that the page holds.  So a token that stays on its page keeps its code unless the scale
+ * grows.  A token from another page with a NaN code or a scale that is not
+ * finite leaves a scale that is not finite, as in mi_decode_kv_append.
+ * Positions from lens[b] + n on hold no token of the sequence afterwards.
+ * max_tokens: the most that a sequence keeps.  batch->cu NULL: one token each.
+ * A page that the kept tokens come to or lie on must belong to one sequence and
+ * be in its table once.
+ */
+mi_decode_status_t mi_decode_kv_keep(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                     const mi_decode_batch_t* batch, const int32_t* keep,
+                                     void* stream);
+
+/*
+ * Page dst[i] becomes a copy of page src[i], codes and scales of all heads, for
+ * 0 <= i < pairs.  A pair with a page outside 0 .. pages - 1, or of a page with
+ * itself, is skipped.  A page may be the source of several pairs; one that is
+ * the destination of a pair must be in no other pair of the call (what it holds
+ * afterwards is not defined then).
+ */
+mi_decode_status_t mi_decode_kv_copy(mi_decode_handle_t h, const mi_decode_cache_t* cache,
+                                     const int32_t* src, const int32_t* dst, int64_t pairs,
+                                     void* stream);
+
+/*
+ * For each row m of x [M][K], with r the row of `residual` (or nothing):
+ *   t = round(x + r) in dtype,            which goes to `total`,
+ *   y = t / sqrt(mean(t^2) + eps) * weight,
+ *   scales[m][j] = max |y[k]| / 448        over 128 j <= k < 128 (j + 1), k < K,
+ *   codes[m][k] = e4m3(y[k] / scales[m][k / 128])   to nearest even, 0 where the scale is 0.
+ * Sums are binary32, and the square root's argument keeps its bits where squares
+ * would leave binary32.  A block with a y that is not finite has a scale that
+ * is not finite, so that it reads as non-finite rather than wrong.
+ *   x, residual, total: of type dtype, rows ldx, ldr and ldt elements apart.
+ *   residual NULL: t is x, and total must be NULL; total NULL: it is not wanted.
+ *   weight [K] of type dtype, or NULL for 1.
+ *   codes: e4m3 bytes, rows ldc >= K apart; scales: binary32, rows
+ *   lds >= ceil(K / 128) apart.  eps: not negative, finite.
+ * total may be x or residual themselves (the same pointer and row distance);
+ * outputs may not overlap anything else.  Any alignment to elements is taken.
+ * M == 0 or K == 0: nothing is done.
+ */
+mi_decode_status_t mi_decode_rms_norm_f8(mi_decode_handle_t h, mi_decode_dtype_t dtype, int64_t M,
+                                         int64_t K, const void* x, int64_t ldx,
+                                         const void* residual, int64_t ldr, const void* weight,
+                                         float eps, void* codes, int64_t ldc, float* scales,
+                                         int64_t lds, void* total, int64_t ldt, void* stream);
+
+/*
+ * y[m][n] = round( sum_j (xs[m][j] * ws[n / 128][j]) * sum_k x[m][k] w[n][k] + bias[n] )
+ * with the inner sum over 128 j <= k < min(128 (j + 1), K): products of e4m3
+ * values, sums and the product of two scales in binary32, one rounding to dtype.
+ *   x [M][K] and w [N][K]: e4m3 bytes, rows ldx and ldw >= K apart.
+ *   xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]: binary32, rows
+ *   ldxs and ldws apart.  bias [N] of type dtype, or NULL.  y: rows ldy >= N apart.
+ * Any alignment to elements is taken; rows of x and w that begin at multiples
+ * of 16 bytes are faster.  M == 0 or N == 0: nothing is done; K == 0: y = bias, or 0.
+ * y must not overlap any input.
+ */
+mi_decode_status_t mi_decode_f8_linear(mi_decode_handle_t h, mi_decode_dtype_t dtype, int64_t M,
+                                       int64_t N, int64_t K, const void* x, int64_t ldx,
+                                       const float* xs, int64_t ldxs, const void* w, int64_t ldw,
+                                       const float* ws, int64_t ldws, const void* bias, void* y,
+                                       int64_t ldy, void* stream);
 
 #ifdef __cplusplus
 }
