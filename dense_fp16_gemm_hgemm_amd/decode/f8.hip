@@ -281,6 +281,134 @@ __global__ __launch_bounds__(64 * WM * WN) void f8_tile_kernel(F8Args p, int who
       store4<BF16>(p, m0 + wm * TM + 16 * m + r, n0 + wn * TN + 16 * n + 4 * g, acc[m][n], whole);
 }
 
+// 256 x 256 tiles for eight waves in two groups that take turns at the matrix
+// pipes: in each phase one group multiplies a block of 128 columns while the
+// other reads its operands of its next block and issues copies.  Group g owns
+// token rows 128 g .. 128 g + 127, its wave w weight rows 64 w .. 64 w + 63.
+// Block kb is multiplied by group 0 in phase 2 kb, by group 1 in phase 2 kb + 1.
+// Weights, scales and half of a group's tokens are read in the phase before, the
+// other half while the first is multiplied.  Both operands have two stages: w and
+// group 0's half of x are free after phase 2 kb, and group 0 refills them in
+// phase 2 kb + 1; group 1's half is free after that, and group 1 refills it in
+// phase 2 kb + 2.  Each waits for its copies at the end of its next
+// multiplication, before the barrier behind which they are first read.
+template <bool BF16>
+__global__ __launch_bounds__(512) void f8_turns_kernel(F8Args p, int whole) {
+  constexpr int BM = 256, BN = 256, FM = 8, FN = 4, XB = BM * 128, WB = BN * 128, STAGE = XB + WB + 4 * BM + 256;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = wave >> 2, w4 = wave & 3, r = lane & 15, g = lane >> 4;
+  const int KB = (p.K + 127) >> 7;
+  int tm, tn;
+  tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int xrows = min(BM, p.M - m0), wrows = min(BN, p.N - n0), b0 = n0 / 128, brows = (n0 + wrows - 1) / 128 - b0 + 1;
+  const u32x4 rx = raw_rsrc(p.x + m0 * p.ldx, (uint32_t)((xrows - 1) * p.ldx + p.K));
+  const u32x4 rw = raw_rsrc(p.w + n0 * p.ldw, (uint32_t)((wrows - 1) * p.ldw + p.K));
+  const u32x4 rxs = raw_rsrc(p.xs + m0 * p.ldxs, (uint32_t)(4 * ((xrows - 1) * p.ldxs + KB)));
+  const u32x4 rws = raw_rsrc(p.ws + b0 * p.ldws, (uint32_t)(4 * ((brows - 1) * p.ldws + KB)));
+  const uint32_t base = lds_at(lds);
+  // A copy is 8 rows; a lane's row of it, and its 16-byte piece in even and odd
+  // ones.  Rows past the tile's end read past the descriptor's, so does a piece past K.
+  const int crow = lane >> 3, ch0 = (lane & 7) ^ (lane >> 4), ch1 = ch0 ^ 4;
+  const uint32_t x0 = (uint32_t)(crow * p.ldx + 16 * ch0), x1 = (uint32_t)(crow * p.ldx + 16 * ch1);
+  const uint32_t w0 = (uint32_t)(crow * p.ldw + 16 * ch0), w1 = (uint32_t)(crow * p.ldw + 16 * ch1);
+  auto copy_x = [&](int half, int kb) {
+    const bool in0 = 128 * kb + 16 * ch0 < p.K, in1 = 128 * kb + 16 * ch1 < p.K;
+    const uint32_t to = base + (kb & 1) * STAGE;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int blk = 16 * half + 4 * w4 + i;
+      copy16(rx, i & 1 ? (in1 ? x1 : kOutside) : (in0 ? x0 : kOutside), (uint32_t)(8 * blk * p.ldx) + 128u * kb, to + 1024 * blk);
+    }
+    if (w4 < 2) {
+      const int row = 128 * half + 64 * w4 + lane;
+      copy4(rxs, row < xrows && kb < KB ? (uint32_t)(4 * row * p.ldxs) : kOutside, 4u * kb, to + XB + WB + 4 * (128 * half + 64 * w4));
+    }
+  };
+  auto copy_w = [&](int kb) {
+    const bool in0 = 128 * kb + 16 * ch0 < p.K, in1 = 128 * kb + 16 * ch1 < p.K;
+    const uint32_t to = base + (kb & 1) * STAGE;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int blk = 8 * w4 + i;
+      copy16(rw, i & 1 ? (in1 ? w1 : kOutside) : (in0 ? w0 : kOutside), (uint32_t)(8 * blk * p.ldw) + 128u * kb, to + XB + 1024 * blk);
+    }
+    if (w4 == 3) copy4(rws, lane < brows && kb < KB ? (uint32_t)(4 * lane * p.ldws) : kOutside, 4u * kb, to + XB + WB + 4 * BM);
+  };
+  auto landed = []() { __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xf << 8)); };  // vmcnt(0)
+
+  const int sw = (r >> 1) & 7, p0 = 16 * (g ^ sw), p1 = p0 ^ 64;
+  const uint8_t* xat = lds + (128 * grp + r) * 128;
+  const uint8_t* wat = lds + XB + (64 * w4 + r) * 128;
+  u32x4 xf[4][2], wf[FN][2];
+  float sc[FM];
+  auto read_x = [&](const uint8_t* at, int m) {
+    xf[m & 3][0] = *reinterpret_cast<const u32x4*>(at + 2048 * m + p0);
+    xf[m & 3][1] = *reinterpret_cast<const u32x4*>(at + 2048 * m + p1);
+  };
+  auto read = [&](int kb) {
+    const int st = (kb & 1) * STAGE;
+    const float* scales = reinterpret_cast<const float*>(lds + st + XB + WB);
+    const float ws = scales[BM + w4 / 2];
+#pragma unroll
+    for (int n = 0; n < FN; ++n) {
+      wf[n][0] = *reinterpret_cast<const u32x4*>(wat + st + 2048 * n + p0);
+      wf[n][1] = *reinterpret_cast<const u32x4*>(wat + st + 2048 * n + p1);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) read_x(xat + st, m);
+#pragma unroll
+    for (int m = 0; m < FM; ++m) sc[m] = scales[128 * grp + 16 * m + r] * ws;
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](int kb) {
+    const uint8_t* at = xat + (kb & 1) * STAGE;
+    __builtin_amdgcn_s_setprio(1);
+    f32x4 d[3];
+    auto add = [&](int i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[i / FN][i % FN][e] = __builtin_fmaf(d[i % 3][e], sc[i / FN], acc[i / FN][i % FN][e]);
+    };
+#pragma unroll
+    for (int i = 0; i < FM * FN; ++i) {
+      const int m = i / FN, n = i % FN;
+      d[i % 3] = mma(wf[n][0], wf[n][1], xf[m & 3][0], xf[m & 3][1]);
+      if (i >= 2) add(i - 2);
+      if (n == FN - 1 && m + 4 < FM) read_x(at, m + 4);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(FM * FN - 2), add(FM * FN - 1);
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  copy_x(grp, 0);
+  if (grp == 0) copy_w(0);
+  landed();
+  __syncthreads();
+  if (grp == 1) __syncthreads();  // phase -1
+  for (int kb = 0; kb < KB; ++kb) {
+    copy_x(grp, kb + 1);
+    if (grp == 0) copy_w(kb + 1);
+    read(kb);
+    __syncthreads();
+    multiply(kb);
+    landed();
+    __syncthreads();
+  }
+  if (grp == 0) __syncthreads();
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      store4<BF16>(p, m0 + 128 * grp + 16 * m + r, n0 + 64 * w4 + 16 * n + 4 * g, acc[m][n], whole);
+}
+
 // ----------------------------------------------------------------- choice --
 
 template <bool BF16, int MT, int NT, int U>
@@ -317,6 +445,11 @@ hipError_t pick(const F8Args& a, hipStream_t s) {
   if (a.M <= 16) return few<BF16, 1, 1, 2>(a, whole, s);
   if (a.M <= 32) return few<BF16, 2, 1, 2>(a, whole, s);
   if (a.M <= 64 || !tiled) return few<BF16, 4, 1, 1>(a, whole, s);
+  if (a.M >= 256 && (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256) >= a.cus / 2) {
+    const int64_t all = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+    if (all > INT32_MAX) return hipErrorInvalidConfiguration;
+    return launch(f8_turns_kernel<BF16>, dim3((unsigned)all), 512, 0, s, a, whole);
+  }
   return tiles<BF16, 128, 128, 2, 2>(a, whole, s);
 }
 
