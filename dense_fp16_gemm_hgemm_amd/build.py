@@ -58,9 +58,10 @@ DEVICE = ["--offload-arch=" + ARCH,
           "-Wno-unused-command-line-argument"]
 
 
-# Attention rescales its accumulators between matrix products: with those in
-# ordinary registers there are no copies out of and into accumulator registers.
-EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in ("attend.hip", "attend_tile.hip")}
+# Attention rescales its accumulators between matrix products, and block scales
+# enter after each: with those in ordinary registers there are no copies out of
+# and into accumulator registers.
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in ("attend.hip", "attend_tile.hip", "f8.hip")}
 
 
 def _compile_cmds(folder=CSRC, prefix=""):

@@ -38,7 +38,8 @@ SIZES = [
     (1, 1, 16), (1, 64, 128), (1, 130, 144), (1, 4096, 4096), (2, 300, 272), (16, 257, 1024), (17, 128, 400), (31, 1000, 640),
     (33, 257, 2048), (64, 500, 1040), (65, 128, 128), (66, 129, 144), (77, 5003, 4072), (100, 300, 4096), (127, 255, 272),
     (128, 128, 256), (129, 260, 384), (200, 1536, 2048), (256, 256, 2048), (257, 700, 4096), (511, 1030, 528), (600, 4096, 256),
-    (1025, 520, 1152), (1, 300, 17), (3, 40, 33), (20, 200, 1001), (70, 300, 515), (300, 140, 999), (5, 70, 1), (40, 9, 15),
+    (1025, 520, 1152), (300, 14000, 260), (1100, 4000, 136), (2100, 4100, 400), (10, 9000, 300), (30, 9000, 268), (60, 9000, 1028),
+    (70, 8000, 392), (90, 300, 4092), (600, 9000, 140), (1, 300, 17), (3, 40, 33), (20, 200, 1001), (70, 300, 515), (300, 140, 999), (5, 70, 1), (40, 9, 15),
 ]
 
 
