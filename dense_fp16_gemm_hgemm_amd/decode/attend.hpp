@@ -226,7 +226,7 @@ __device__ inline void store_row(const AttendArgs& p, int first, int r, int h, i
 }
 
 // A part in the workspace: sums of ROWS x D, then m and l of each row.
-constexpr uint32_t part_bytes(int rows, int D) { return 4 * (uint32_t)rows * (D + 2); }
+__host__ __device__ constexpr uint32_t part_bytes(int rows, int D) { return 4 * (uint32_t)rows * (D + 2); }
 
 // Counts a workgroup in whose part is stored; true in the last of `parts`.
 //

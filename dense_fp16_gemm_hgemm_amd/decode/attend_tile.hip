@@ -58,6 +58,64 @@ __device__ inline void schedule_reads() {
   __builtin_amdgcn_sched_group_barrier(0x8, AHEAD, 0);
 }
 
+// The parts of a tree's items.  Sequences differ in length, and their drafts all
+// see the whole of it, so an item (row block, sequence, head) has as many parts as
+// its length asks for: `chunk` stages to a part, and `chunk` so that there are about
+// as many parts as compute units.  A workgroup finds its item by a scan over the
+// row blocks, 64 at a time.  Of t stages in all, t / chunk + items parts are there
+// at most, and as an item in parts has more than chunk stages, 2 t / chunk of those
+// have a place in the workspace.
+__host__ __device__ inline int line_parts(int cus, uint32_t part) {
+  const int room = (int)(MI_DECODE_WORKSPACE_BYTES / part / 2);
+  return cus < room ? cus : room;
+}
+__device__ inline bool place_on_line(const AttendArgs& p, int G, int blocks, int block_rows, uint32_t part, Block<kStage>& blk,
+                                     int& h, int& j, int& parts, int& item, int& slot) {
+  constexpr int kLeast = 4;  // stages of a part: joining it costs about two
+  const int lane = threadIdx.x & 63, H = p.cache.kv_heads, pairs = p.batch.batch * blocks;
+  auto sum_up_to = [&](int x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(x, d);
+      if (lane >= d) x += o;
+    }
+    return x;
+  };
+  Block<kStage> mine;
+  int64_t total = 0;
+  int at = 0;
+  while (true) {
+    mine = block_of<kStage, true>(p, G, block_rows, blocks, at + lane, pairs);
+    total += lane_value(sum_up_to(mine.tiles), 63);
+    if (at + 64 >= pairs) break;
+    at += 64;
+  }
+  const int want = line_parts(p.cus, part);
+  const int chunk = max(kLeast, (int)((total * H + want - 1) / want));
+  int before = 0, slots = 0;
+  const bool again = at > 0;
+  for (at = 0; at < pairs; at += 64) {
+    if (again) mine = block_of<kStage, true>(p, G, block_rows, blocks, at + lane, pairs);
+    // a block without rows has a part too: its workgroup writes that nothing is joined
+    const int n = at + lane < pairs ? max(1, (mine.tiles + chunk - 1) / chunk) : 0;
+    const int upto = sum_up_to(n * H), used = sum_up_to(n > 1 ? n * H : 0);
+    const uint64_t m = __ballot(before + upto > (int)blockIdx.x);
+    if (m) {
+      const int l = __builtin_ctzll(m);
+      blk = mine.of_lane(l);
+      parts = lane_value(n, l);
+      const int off = (int)blockIdx.x - before - (lane_value(upto, l) - parts * H);
+      h = off / parts, j = off % parts;
+      item = (at + l) * H + h;
+      slot = parts > 1 ? slots + lane_value(used, l) - parts * H + h * parts : 0;
+      if (blk.tiles == 0) parts = 0;
+      return true;
+    }
+    before += lane_value(upto, 63), slots += lane_value(used, 63);
+  }
+  return false;
+}
+
 template <int CODE, int D, int NW, bool TREE>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(AttendArgs p, int blocks, int splits) {
   constexpr int ROWS = 32 * NW, KS = D / 16, DT = D / 32, T = 64 * NW;
@@ -78,11 +136,17 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
   // with a multiple of 8 they share an XCD's L2.  The last rows, which see
   // most, come first.
   const int heads = p.batch.batch * H, bh = blockIdx.x % heads, rest = blockIdx.x / heads;
-  const int j = rest % splits, rb = blocks - 1 - rest / splits, h = bh % H;
-  const Block<kStage> blk = block_of<kStage, TREE>(p, G, ROWS, blocks, bh / H * blocks + rb, p.batch.batch * blocks);
-  const int parts = blk.tiles == 0 ? 0 : min(splits, max(1, blk.tiles / 4)), item = rb * heads + bh;
-  if (splits > 1 && j == 0 && tid == 0) {
-    const uint32_t at = (uint32_t)(item * splits) * kPart;
+  int j = rest % splits, h = bh % H, parts = 1, item, slot;
+  Block<kStage> blk;
+  if (TREE && p.join) {
+    if (!place_on_line(p, G, blocks, ROWS, kPart, blk, h, j, parts, item, slot)) return;
+  } else {
+    const int rb = blocks - 1 - rest / splits;
+    blk = block_of<kStage, TREE>(p, G, ROWS, blocks, bh / H * blocks + rb, p.batch.batch * blocks);
+    parts = blk.tiles == 0 ? 0 : min(splits, max(1, blk.tiles / 4)), item = rb * heads + bh, slot = item * splits;
+  }
+  if ((TREE ? p.join != nullptr : splits > 1) && j == 0 && tid == 0) {
+    const uint32_t at = (uint32_t)slot * kPart;
     p.join[item] = parts > 1 ? JoinItem{blk.first, blk.r0, blk.rows, h, parts, at, at + kPart, kPart} : JoinItem{};
   }
   if (j >= parts) return;
@@ -418,7 +482,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attend_tile_kernel(
     return;
   }
   const auto parts_at = __builtin_amdgcn_make_buffer_rsrc(p.ws, (short)0, (int)MI_DECODE_WORKSPACE_BYTES, kRsrcWord3);
-  const uint32_t to = (uint32_t)(item * splits + j) * kPart;
+  const uint32_t to = (uint32_t)(slot + j) * kPart;
   if (in) {
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -446,9 +510,17 @@ hipError_t run_as(const AttendArgs& a, hipStream_t s) {
   const int64_t stages = a.max_len / kStage + 1;
   if (splits > stages / 4) splits = stages / 4 > 0 ? stages / 4 : 1;
   if (items * splits * part_bytes(ROWS, D) > MI_DECODE_WORKSPACE_BYTES) splits = 1;
+  AttendArgs b = a;
+  int64_t grid = items * splits;
+  if (TREE) {
+    splits = 1, grid = items;
+    // a part has four stages at least, and the list of joins has its length
+    if (stages <= 4 || items > kJoins) b.join = nullptr;
+    else grid = items + line_parts(a.cus, part_bytes(ROWS, D));
+  }
   const hipError_t e =
-      launch(attend_tile_kernel<CODE, D, NW, TREE>, (unsigned)(items * splits), 64 * NW, 0, s, a, (int)blocks, (int)splits);
-  return e != hipSuccess || splits == 1 ? e : launch_join(a, (int)items, ROWS, s);
+      launch(attend_tile_kernel<CODE, D, NW, TREE>, (unsigned)grid, 64 * NW, 0, s, b, (int)blocks, (int)splits);
+  return e != hipSuccess || (TREE ? !b.join : splits == 1) ? e : launch_join(b, (int)items, ROWS, s);
 }
 
 template <int CODE, int D, int NW>

@@ -252,3 +252,24 @@ def test_refusals(d):
         call(bits, window=-1)
     with pytest.raises(decode.DecodeError):
         call(bits, scale=math.inf)
+
+
+@pytest.mark.parametrize("D, Hkv, new", [(128, 8, 64), (64, 2, 64), (256, 2, 130)])
+def test_very_uneven_lengths(d, D, Hkv, new):
+    """Many rows, one long sequence among short, empty and middling ones: parts by length, some joined and some not."""
+    r = random.Random(D)
+    n = [r.randint(1, new) for _ in range(12)]
+    n[0], n[5], n[7] = new, 0, new
+    lens = [a + c for a, c in zip(n, [20000, 3, 0, 700, 64, 100, 2000, 10000, 1, 63, 5000, 257])]
+    run(d, lens, n, 4 * Hkv, Hkv, D, 64, torch.int8, torch.float16, seed=D, window=0)
+    run(d, lens, n, 4 * Hkv, Hkv, D, 64, E4M3, torch.bfloat16, seed=D, window=3000, sinks=100)
+
+
+def test_more_row_blocks_than_lanes_with_many_rows(d):
+    """Over 64 row blocks on the line, most of them short."""
+    r = random.Random(2)
+    n = [r.randint(0, 40) for _ in range(100)]
+    n[3] = n[80] = 40
+    lens = [a + r.choice((0, 5, 200, 900)) for a in n]
+    lens[3], lens[80] = 6000, 9000
+    run(d, lens, n, 8, 2, 64, 16, seed=62)
