@@ -606,7 +606,18 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
   // rows 32 and 24).  256 channels, 1 x 8 items against 8192 tokens: 128 rows 42
   // and 50, 256 rows 62 and 63, 512 rows 99 and 95; with 32 x 8 items against
   // 4096 tokens 64 rows 194 and 280, 80 rows 313 and 280, 512 rows 1397 and 1143.
-  if (rows > (a.cache.head_dim == 256 ? 511 : 64)) return launch_attend_tile(a, s);
+  bool tile = rows > (a.cache.head_dim == 256 ? 511 : 64);
+  // Trees of a batch differ in size, and rows that no sequence has cost nothing here:
+  // by the rows that a sequence has on the mean.  us here and there, 32 sequences to
+  // 2048 tokens: 64 channels, 128 rows each 59 and 82, 192 rows 102 and 76; 128
+  // channels, 80 rows 121 and 80, up to 128 rows and 66 on the mean (to 12000 tokens)
+  // 84 and 108; 256 channels, 80 rows 180 and 166, 256 rows 428 and 334, up to 256
+  // rows and 116 on the mean (to 8000 tokens) 189 and 263.
+  if (a.seen && rows > 64) {
+    const int64_t mean = (int64_t)(a.q_heads / a.cache.kv_heads) * a.batch.tokens / a.batch.batch;
+    tile = a.cache.head_dim == 64 ? mean > 150 : a.cache.head_dim == 128 ? mean > 68 : tile || 5 * mean > 3 * rows;
+  }
+  if (tile) return launch_attend_tile(a, s);
   return a.cache.code == MI_DECODE_INT8 ? dims_of<MI_DECODE_INT8>(a, s) : dims_of<MI_DECODE_E4M3>(a, s);
 }
 

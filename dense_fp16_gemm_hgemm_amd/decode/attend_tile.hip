@@ -60,19 +60,18 @@ __device__ inline void schedule_reads() {
 
 // The parts of a tree's items.  Sequences differ in length, and their drafts all
 // see the whole of it, so an item (row block, sequence, head) has as many parts as
-// its length asks for: `chunk` stages to a part, and `chunk` so that there are about
-// as many parts as compute units.  A workgroup finds its item by a scan over the
-// row blocks, 64 at a time.  Of t stages in all, t / chunk + items parts are there
-// at most, and as an item in parts has more than chunk stages, 2 t / chunk of those
-// have a place in the workspace.
-__host__ __device__ inline int line_parts(int cus, uint32_t part) {
-  const int room = (int)(MI_DECODE_WORKSPACE_BYTES / part / 2);
-  return cus < room ? cus : room;
-}
+// its length asks for, of `chunk` stages at most.  A workgroup finds its part by a
+// scan over the row blocks, 64 at a time; those of items in parts come first, as
+// the others are the shorter ones and fill what is left (32 sequences to 12000
+// tokens with up to 64 drafts: one item to a workgroup 428 us, parts for one round
+// of workgroups in the items' order 137, so 112; one line that the workgroups cut
+// into equal pieces 163, where the loop over a piece's items takes 20 % longer for
+// each stage).
+constexpr int kLeast = 4;  // stages of a part: joining it costs about two
+__host__ __device__ inline int room_of(uint32_t part) { return (int)(MI_DECODE_WORKSPACE_BYTES / part); }
 __device__ inline bool place_on_line(const AttendArgs& p, int G, int blocks, int block_rows, uint32_t part, Block<kStage>& blk,
                                      int& h, int& j, int& parts, int& item, int& slot) {
-  constexpr int kLeast = 4;  // stages of a part: joining it costs about two
-  const int lane = threadIdx.x & 63, H = p.cache.kv_heads, pairs = p.batch.batch * blocks;
+  const int lane = threadIdx.x & 63, H = p.cache.kv_heads, pairs = p.batch.batch * blocks, room = room_of(part);
   auto sum_up_to = [&](int x) {
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -82,23 +81,56 @@ __device__ inline bool place_on_line(const AttendArgs& p, int G, int blocks, int
     return x;
   };
   Block<kStage> mine;
+  int loaded = -1;
+  auto load = [&](int at) {
+    if (at != loaded) mine = block_of<kStage, true>(p, G, block_rows, blocks, at + lane, pairs);
+    loaded = at;
+  };
+  // a block without rows has a part too: its workgroup writes that nothing is joined
+  auto parts_of = [&](int at, int chunk) { return at + lane < pairs ? max(1, (mine.tiles + chunk - 1) / chunk) : 0; };
   int64_t total = 0;
-  int at = 0;
-  while (true) {
-    mine = block_of<kStage, true>(p, G, block_rows, blocks, at + lane, pairs);
+  int most = 0;
+  for (int at = 0; at < pairs; at += 64) {
+    load(at);
     total += lane_value(sum_up_to(mine.tiles), 63);
-    if (at + 64 >= pairs) break;
-    at += 64;
+    most = max(most, mine.tiles);
   }
-  const int want = line_parts(p.cus, part);
-  const int chunk = max(kLeast, (int)((total * H + want - 1) / want));
-  int before = 0, slots = 0;
-  const bool again = at > 0;
-  for (at = 0; at < pairs; at += 64) {
-    if (again) mine = block_of<kStage, true>(p, G, block_rows, blocks, at + lane, pairs);
-    // a block without rows has a part too: its workgroup writes that nothing is joined
-    const int n = at + lane < pairs ? max(1, (mine.tiles + chunk - 1) / chunk) : 0;
-    const int upto = sum_up_to(n * H), used = sum_up_to(n > 1 ? n * H : 0);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) most = max(most, __shfl_xor(most, d));
+  // Whole items, parts for one round of workgroups, or for two, by how many stages
+  // it takes until the last one ends; starting a part costs about three, joining four.
+  const float cus = (float)p.cus, items = (float)(pairs * H), all = (float)(total * H);
+  auto until = [&](float chunk, float parts) { return parts <= cus ? chunk + 3.f : (all + 3.f * parts) / cus + 0.5f * chunk; };
+  auto chunk_of = [&](int want) { return min(most, max(kLeast, (int)((total * H + want - 1) / want))); };
+  int chunk = most;
+  float least = until((float)most, items);
+  for (int rounds = 2; rounds >= 1; --rounds) {
+    const int c = chunk_of(rounds * p.cus);
+    const float u = until((float)c, all / (float)c + (rounds == 1 ? 0.f : items)) + 4.f;
+    if (c > 0 && u < least) chunk = c, least = u;
+  }
+  // Of t stages, an item in parts has more than chunk and so fewer than 2 tiles / chunk
+  // parts: with t / chunk at most half the room all have a place.
+  int many = 0;  // parts of items in parts
+  auto count = [&]() {
+    many = 0;
+    for (int at = 0; at < pairs; at += 64) {
+      load(at);
+      const int n = parts_of(at, chunk);
+      many += lane_value(sum_up_to(n > 1 ? n * H : 0), 63);
+    }
+  };
+  chunk = max(chunk, 1);
+  count();
+  if (many > room) {
+    chunk = max(chunk_of(min(p.cus, room / 2)), 1);
+    count();
+  }
+  const bool first = (int)blockIdx.x < many;  // of an item in parts
+  int before = first ? 0 : many;
+  for (int at = 0; at < pairs; at += 64) {
+    load(at);
+    const int n = parts_of(at, chunk), upto = sum_up_to((n > 1) == first ? n * H : 0);
     const uint64_t m = __ballot(before + upto > (int)blockIdx.x);
     if (m) {
       const int l = __builtin_ctzll(m);
@@ -107,11 +139,11 @@ __device__ inline bool place_on_line(const AttendArgs& p, int G, int blocks, int
       const int off = (int)blockIdx.x - before - (lane_value(upto, l) - parts * H);
       h = off / parts, j = off % parts;
       item = (at + l) * H + h;
-      slot = parts > 1 ? slots + lane_value(used, l) - parts * H + h * parts : 0;
+      slot = (int)blockIdx.x - j;
       if (blk.tiles == 0) parts = 0;
       return true;
     }
-    before += lane_value(upto, 63), slots += lane_value(used, 63);
+    before += lane_value(upto, 63);
   }
   return false;
 }
@@ -514,9 +546,9 @@ hipError_t run_as(const AttendArgs& a, hipStream_t s) {
   int64_t grid = items * splits;
   if (TREE) {
     splits = 1, grid = items;
-    // a part has four stages at least, and the list of joins has its length
-    if (stages <= 4 || items > kJoins) b.join = nullptr;
-    else grid = items + line_parts(a.cus, part_bytes(ROWS, D));
+    // the list of joins has its length
+    if (stages <= kLeast || items > kJoins) b.join = nullptr;
+    else grid = items + 2 * a.cus;
   }
   const hipError_t e =
       launch(attend_tile_kernel<CODE, D, NW, TREE>, (unsigned)grid, 64 * NW, 0, s, b, (int)blocks, (int)splits);

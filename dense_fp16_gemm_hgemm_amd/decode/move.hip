@@ -49,86 +49,162 @@ __device__ inline u32x4 rescaled(u32x4 w, double ratio) {
   return o;
 }
 
-// One workgroup moves the kept tokens of a sequence in one head of K or of V,
-// page by page in the order of positions: a token comes from its own place or a
-// later one, so what a page reads no earlier page has written.
+// The largest of sixteen codes' magnitudes times by, as bits.
+template <int CODE>
+__device__ inline uint64_t largest(u32x4 w, double by) {
+  uint64_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = max(m, abs_bits(from_code<CODE>((uint8_t)(w[e / 4] >> (8 * (e % 4)))) * by));
+  return m;
+}
+
+// Every load before it has brought its value when a wave passes, so that what
+// other waves store behind it cannot be what is loaded.
+__device__ inline void all_read() {
+  __builtin_amdgcn_s_waitcnt((0x7 << 4) | (0xf << 8));  // vmcnt(0)
+  __syncthreads();
+}
+
+// One workgroup moves the kept tokens of a sequence in one head of K or of V.
+//
+// Where all of them fit into its registers they are all read before any is
+// written, and the pages' maxima lie in shared memory: one chain of dependent
+// loads (lengths, index, pages, codes and scales).  Otherwise page by page in the
+// order of positions: a token comes from its own place or a later one, so what a
+// page reads no earlier page has written.
+//
+// Bound: those latencies, 4 us for one sequence and, 128 sequences with paths of a
+// dozen tokens over pages of 16, 9.7 us in eight rounds of workgroups (page by page,
+// with its loads for each page in turn, 14.6).
 template <int CODE>
 __global__ __launch_bounds__(256) void keep_kernel(KeepArgs p) {
-  __shared__ uint64_t part[4];
+  constexpr int KEEP = 2, PAGES = KEEP * 64 / 16 + 1;  // pages of 16 that KEEP rows a thread of 64 channels lie on
+  __shared__ unsigned long long top[PAGES];
   const int H = p.cache.kv_heads, D = p.cache.head_dim, ps = p.cache.page_size;
   const int b = blockIdx.x / (2 * H), h = blockIdx.x % (2 * H) >> 1, is_v = blockIdx.x & 1;
   const Span sp = span_of(p.batch, b);
+  const int64_t held_now = p.batch.lens[b];
   const int n = min(sp.n, p.batch.max_tokens);
   if (n <= 0) return;
   const int64_t cap = (int64_t)p.batch.table_cols * ps;
-  const int64_t past = min(max((int64_t)p.batch.lens[b], (int64_t)0), cap);
+  const int64_t past = min(max(held_now, (int64_t)0), cap);
   uint8_t* codes = static_cast<uint8_t*>(is_v ? p.cache.v : p.cache.k);
   float* scales = is_v ? p.cache.v_scale : p.cache.k_scale;
   const int per = D / 16, rows = 256 / per, r0 = threadIdx.x / per, c = threadIdx.x % per;
   auto row_at = [&](int page, int slot) {
     return reinterpret_cast<u32x4*>(codes + (((int64_t)page * H + h) * ps + slot) * D) + c;
   };
+  auto page_at = [&](int64_t pos) { return page_of(p.cache, p.batch, b, (int)min(pos / ps, (int64_t)p.batch.table_cols)); };
+  // where token i comes from: its page, or `page` and its own slot
+  struct Source {
+    int page, slot;
+  };
+  auto source = [&](int i, int page) {
+    const int k = p.keep[sp.first + i];
+    const int64_t pos = past + k;
+    const int from = k < i ? -1 : page_at(pos);
+    return from < 0 ? Source{page, (int)((past + i) % ps)} : Source{from, (int)(pos % ps)};
+  };
+  // a page's new scale from the bits of the largest that comes
+  struct Scale {
+    double s;
+    bool grows;
+  };
+  auto scale_of = [&](uint64_t m, float old) {
+    const double mine = __builtin_bit_cast(double, m) * (1. / kQmax<CODE>);
+    const bool grows = abs_bits(mine) > abs_bits(old);
+    return Scale{grows ? mine : old, grows};
+  };
+  // the codes of a token as they are on a page of scale s
+  auto changed = [&](u32x4 w, double by, double s, bool moved_in) {
+    if (s == 0.) return u32x4{0, 0, 0, 0};
+    const double ratio = by / s;
+    return ratio != 1. && moved_in ? rescaled<CODE>(w, ratio) : w;
+  };
+  const int64_t upto = min(past + n, cap), start0 = past - past % ps;
 
-  const int64_t upto = min(past + n, cap);
-  for (int64_t start = past - past % ps; start < upto; start += ps) {
-    const int page = page_of(p.cache, p.batch, b, (int)(start / ps));
+  if (n <= KEEP * rows) {
+    const int pages = (int)((upto - 1 - start0) / ps) + 1;
+    if ((int)threadIdx.x < PAGES) top[threadIdx.x] = 0;
+    u32x4 w[KEEP];
+    int to[KEEP], slot[KEEP], in[KEEP];  // page and slot, which of the pages, and whether the code comes from another
+    bool stays[KEEP], other[KEEP];
+    float by[KEEP], old[KEEP];
+    for (int k = 0; k < KEEP; ++k) to[k] = -1;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) {
+      const int i = r0 + k * rows;
+      if (i >= n || past + i >= cap) continue;
+      to[k] = page_at(past + i);
+      if (to[k] < 0) continue;
+      const Source s = source(i, to[k]);
+      slot[k] = (int)((past + i) % ps), in[k] = (int)((past + i - start0) / ps);
+      other[k] = s.page != to[k], stays[k] = !other[k] && s.slot == slot[k];
+      w[k] = *row_at(s.page, s.slot);
+      by[k] = scales[(int64_t)s.page * H + h], old[k] = scales[(int64_t)to[k] * H + h];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+      if (to[k] >= 0 && other[k]) atomicMax(&top[in[k]], (unsigned long long)largest<CODE>(w[k], by[k]));
+    // the first page's scale for the tokens before the path, and every page's to be stored
+    const int mine = (int)threadIdx.x < pages ? page_at(start0 + (int64_t)threadIdx.x * ps) : -1;
+    const float mine_old = mine >= 0 ? scales[(int64_t)mine * H + h] : 0.f;
+    const int first = page_at(start0);
+    const float first_old = first >= 0 ? scales[(int64_t)first * H + h] : 0.f;
+    all_read();
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) {
+      if (to[k] < 0) continue;
+      const Scale s = scale_of(top[in[k]], old[k]);
+      if (s.grows || !stays[k]) *row_at(to[k], slot[k]) = changed(w[k], by[k], s.s, s.grows || other[k]);
+    }
+    if (mine >= 0) {
+      const Scale s = scale_of(top[threadIdx.x], mine_old);
+      if (s.grows) scales[(int64_t)mine * H + h] = (float)s.s;
+    }
+    if (first >= 0) {
+      const Scale s = scale_of(top[0], first_old);
+      if (s.grows)
+        for (int r = r0; r < (int)(past - start0); r += rows) *row_at(first, r) = changed(*row_at(first, r), first_old, s.s, true);
+    }
+    return;
+  }
+
+  for (int64_t start = start0; start < upto; start += ps) {
+    const int page = page_at(start);
     if (page < 0) continue;
     const int lo = (int)(max(start, past) - past), hi = (int)(min(start + ps, upto) - past);  // tokens that come here
     const float old = scales[(int64_t)page * H + h];
-    // where token i comes from: its page, or `page` and its own slot
-    struct Source {
-      int page, slot;
-    };
-    auto source = [&](int i) {
-      const int k = p.keep[sp.first + i];
-      const int64_t pos = past + k;
-      const int from = k < i ? -1 : page_of(p.cache, p.batch, b, (int)min(pos / ps, (int64_t)p.batch.table_cols));
-      return from < 0 ? Source{page, (int)((past + i) % ps)} : Source{from, (int)(pos % ps)};
-    };
+    __syncthreads();  // the last page's maximum has been read
+    if (threadIdx.x == 0) top[0] = 0;
+    __syncthreads();
     uint64_t m = 0;
     for (int i = lo + r0; i < hi; i += rows) {
-      const Source s = source(i);
-      if (s.page == page) continue;
-      const double by = scales[(int64_t)s.page * H + h];
-      const u32x4 w = *row_at(s.page, s.slot);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) m = max(m, abs_bits(from_code<CODE>((uint8_t)(w[e / 4] >> (8 * (e % 4)))) * by));
+      const Source s = source(i, page);
+      if (s.page != page) m = max(m, largest<CODE>(*row_at(s.page, s.slot), scales[(int64_t)s.page * H + h]));
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) m = max(m, (uint64_t)__shfl_xor((unsigned long long)m, d));
-    __syncthreads();  // the last page's maximum has been read
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = m;
+    if (m) atomicMax(&top[0], (unsigned long long)m);
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) m = max(m, part[w]);
-    const double mine = __builtin_bit_cast(double, m) * (1. / kQmax<CODE>);
-    const bool grows = abs_bits(mine) > abs_bits(old);
-    const double s1 = grows ? mine : old;
-
+    const Scale sc = scale_of(top[0], old);
     // tokens in order, `rows` at a time: all of them are read before any is written
     for (int i0 = lo; i0 < hi; i0 += rows) {
       const int i = i0 + r0;
       bool put = false;
       u32x4 w;
       if (i < hi) {
-        const Source s = source(i);
-        const double by = s.page == page ? old : scales[(int64_t)s.page * H + h];
-        put = grows || s.page != page || s.slot != (int)((past + i) % ps);
-        if (put) {
-          w = *row_at(s.page, s.slot);
-          const double ratio = by / s1;
-          if (s1 == 0.) w = u32x4{0, 0, 0, 0};
-          else if (ratio != 1. && (grows || s.page != page)) w = rescaled<CODE>(w, ratio);
-        }
+        const Source s = source(i, page);
+        put = sc.grows || s.page != page || s.slot != (int)((past + i) % ps);
+        if (put)
+          w = changed(*row_at(s.page, s.slot), s.page == page ? old : scales[(int64_t)s.page * H + h], sc.s,
+                      sc.grows || s.page != page);
       }
-      __syncthreads();
+      all_read();
       if (put) *row_at(page, (int)((past + i) % ps)) = w;
     }
-    if (grows) {
-      const int held = (int)(past + lo - start);
-      const double ratio = old / s1;
-      for (int r = r0; r < held; r += rows) *row_at(page, r) = rescaled<CODE>(*row_at(page, r), ratio);
-      if (threadIdx.x == 0) scales[(int64_t)page * H + h] = (float)s1;
+    if (sc.grows) {
+      for (int r = r0; r < (int)(past + lo - start); r += rows) *row_at(page, r) = changed(*row_at(page, r), old, sc.s, true);
+      if (threadIdx.x == 0) scales[(int64_t)page * H + h] = (float)sc.s;
     }
   }
 }
