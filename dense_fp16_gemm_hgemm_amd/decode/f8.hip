@@ -45,7 +45,7 @@ __device__ __forceinline__ void here(f32x4& x) {
 // The N products of a block and their scaled additions: a product's results come
 // 8 to 11 issue slots after it, so its additions follow the next LAG products
 // (right behind the next one each product waits 3 to 6 slots: 8192 x 4096 x 11008
-// 315 us, here LATER).  `more` is what else is done meanwhile, such as reads.
+// 322 us, here 310).  `more` is what else is done meanwhile, such as reads.
 template <int N, typename Mul, typename Add, typename More>
 __device__ __forceinline__ void products(Mul mul, Add add, More more) {
   constexpr int LAG = 3;
@@ -288,6 +288,14 @@ __device__ inline void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& t
 // ring is one block of 128 columns, rows of 128 bytes whose 16-byte pieces are
 // exchanged by (row / 2) % 8, so that eight rows' reads of one piece meet no bank
 // twice.
+//
+// Bound: copies, reads and products side by side, none of them alone.  1024 x 4096
+// x 4096 took 41 us with a stage's copies issued together and 28 with them spread
+// between its products; on the way, at 32, leaving out the copies, the reads or the
+// products (a copy, for timing) left 22, 24 and 26.  Two, three or four stages
+// make no difference.  Copies of what lies in an XCD's cache reach 128 GB/s for a
+// compute unit, from the last-level cache 28, so workgroups that run together on an XCD
+// share rows of tiles (tile_of).
 template <bool BF16, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void f8_tile_kernel(F8Args p, int whole) {
   constexpr int W = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
@@ -416,6 +424,10 @@ __global__ __launch_bounds__(64 * WM * WN) void f8_tile_kernel(F8Args p, int who
 // phase 2 kb + 1; group 1's half is free after that, and group 1 refills it in
 // phase 2 kb + 2.  Each waits for its copies at the end of its next
 // multiplication, before the barrier behind which they are first read.
+//
+// Bound: matrix instructions.  8192 x 4096 x 11008 310 to 316 us, 2340 to 2380 TFLOP/s,
+// where a large library product with one scale for each operand reaches 2590; a
+// scaled addition is four vector instructions to 32 cycles of the matrix pipe.
 template <bool BF16, int BN>
 __global__ __launch_bounds__(512) void f8_turns_kernel(F8Args p, int whole) {
   constexpr int BM = 256, TN = BN / 4, FM = 8, FN = TN / 16, XB = BM * 128, WB = BN * 128, STAGE = XB + WB + 4 * BM + 256;
@@ -520,6 +532,11 @@ __global__ __launch_bounds__(512) void f8_turns_kernel(F8Args p, int whole) {
 // 16 NT weight rows by up to 16 MT tokens to a workgroup whose W waves split K:
 // wave w takes blocks w, w + W, ... through a ring of S stages of its own in
 // shared memory, so that no wave waits for another before the sums are added.
+//
+// Bound: launch and one or two rounds of loads for small weights (1 x 4096 x 4096
+// 6.0 us with weights from memory, 4.9 from the last-level cache), the weights' bytes
+// for large ones (1 x 14336 x 4096 15.3, 3.8 TB/s).  With operands in registers
+// instead, which hold fewer loads in flight, 64 x 4096 x 4096 took 22 us; here 9.8.
 template <bool BF16, int MT, int NT, int S, int W>
 __global__ __launch_bounds__(64 * W) void f8_strip_kernel(F8Args p, int whole) {
   constexpr int SCALES = (MT + 3) / 4, STAGE = 2048 * (MT + NT) + 256 * SCALES, COPIES = 2 * (MT + NT) + SCALES;
@@ -708,7 +725,7 @@ hipError_t pick(const F8Args& a, hipStream_t s) {
   for (int i = 0; i < 6; ++i) {
     const int64_t all = ((int64_t)a.M + kTiles[i].bm - 1) / kTiles[i].bm * (((int64_t)a.N + kTiles[i].bn - 1) / kTiles[i].bn);
     const float us = (float)((all + a.cus - 1) / a.cus) * kTiles[i].us;
-    if (us <= least && (i < 5 || multiple(16))) best = i, least = us;
+    if (us <= least && (i < 5 || multiple(16)) && (i > 0 || a.M <= 64 * 65535)) best = i, least = us;
   }
   switch (best) {
     case 0: return strips<BF16, 4, 2, 2, 6>(a, whole, s);

@@ -99,9 +99,10 @@ struct F8Args {
 };
 
 // Enqueues a kernel and returns its own launch's status: the runtime's last error
-// may be another call's, from before.
+// may be another call's, from before.  A launch counts its threads in 32 bits.
 template <typename... P, typename... A>
 hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t shared, hipStream_t s, A... a) {
+  if ((uint64_t)grid.x * block.x > UINT32_MAX) return hipErrorInvalidConfiguration;
   return [&](P... p) {
     void* args[] = {&p...};
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, shared, s);

@@ -1,5 +1,15 @@
 // Norm with the residual's addition, into 8-bit floats with a scale for 128 columns:
 //   t = round(x + r),  y = t / sqrt(mean t^2 + eps) * g,  s_j = max |y| / 448,  code = rne(y / s_j).
+//
+// One pass: a thread keeps its columns of t in registers, the row's sum of squares
+// is one exchange over its threads, and a block's maximum one over sixteen lanes
+// (sixteen threads hold 128 columns).  y is not rounded before it is divided by the
+// scale.  Above 16384 columns t is read again, from the caches for the most part.
+//
+// Bound: for many rows the bytes, x, r, t and codes at a large copy's rate (8192 x
+// 4096 bf16 57 us as nodes of a graph, 4.1 TB/s of 235 MB; the same read again
+// instead of kept 62, a wave to a row 69).  For few rows launch, one round of
+// loads, the exchanges and the division (1 x 4096 4.2 us, an empty kernel 3.3).
 #include "device.hpp"
 
 namespace mid {
@@ -183,14 +193,21 @@ hipError_t run(const NormArgs& a, hipStream_t s) {
   return launch(norm_kernel<BF16, WIDE, T, C>, dim3((unsigned)((a.M + ROWS - 1) / ROWS)), T < 256 ? 256 : T, 0, s, a);
 }
 
+// Up to 512 rows take many threads with one or two groups of columns each, as
+// the time is one thread's chain; more rows take fewer threads, so that several
+// rows share a compute unit (us for 1, 512 and 8192 rows of 4096 columns: 512 threads
+// 4.2, 7.1, 61; 256 threads 5.1, 7.8, 57.  1 and 512 rows of 8192: 1024 threads 4.9,
+// 10.7; 256 threads 7.8, 12.4.  Of 16384: 1024 threads 7.0, 17.2; 512 threads 8.5, 18.5.
+// 512 rows of 1024: 256 threads 4.6, 64 threads 5.5).
 template <bool BF16, bool WIDE>
 hipError_t pick(const NormArgs& a, hipStream_t s) {
+  const bool few = a.M <= 512;
   if (a.K <= 512) return run<BF16, WIDE, 64, 1>(a, s);
-  if (a.K <= 1024) return run<BF16, WIDE, 64, 2>(a, s);
+  if (a.K <= 1024) return few ? run<BF16, WIDE, 256, 1>(a, s) : run<BF16, WIDE, 64, 2>(a, s);
   if (a.K <= 2048) return run<BF16, WIDE, 256, 1>(a, s);
-  if (a.K <= 4096) return run<BF16, WIDE, 256, 2>(a, s);
-  if (a.K <= 8192) return run<BF16, WIDE, 256, 4>(a, s);
-  if (a.K <= 16384) return run<BF16, WIDE, 512, 4>(a, s);
+  if (a.K <= 4096) return few ? run<BF16, WIDE, 512, 1>(a, s) : run<BF16, WIDE, 256, 2>(a, s);
+  if (a.K <= 8192) return few ? run<BF16, WIDE, 1024, 1>(a, s) : run<BF16, WIDE, 256, 4>(a, s);
+  if (a.K <= 16384) return few ? run<BF16, WIDE, 1024, 2>(a, s) : run<BF16, WIDE, 512, 4>(a, s);
   return run<BF16, WIDE, 1024, 0>(a, s);
 }
 

@@ -267,9 +267,10 @@ mi_decode_status_t mi_decode_kv_attend_tree(mi_decode_handle_t h, const mi_decod
  * on: s' = max(s, max |x| / QMAX) over the tokens x that come from other pages.
  * Codes become round(code * (s_source / s')), 0 where s' is 0, with s' and the
  * ratio in binary64: those that come, and, where s' > s, those of all positions
- * up to lens[b] + n - 1 that the page holds.  So a token that stays on its page keeps its code unless the scale
- * grows.  A token from another page with a NaN code or a scale that is not
- * finite leaves a scale that is not finite, as in mi_decode_kv_append.
+ * up to lens[b] + n - 1 that the page holds.  So a token that stays on its page
+ * keeps its code unless the scale grows.  A token from another page with a NaN
+ * code or a scale that is not finite leaves a scale that is not finite, as in
+ * mi_decode_kv_append.
  * Positions from lens[b] + n on hold no token of the sequence afterwards.
  * max_tokens: the most that a sequence keeps.  batch->cu NULL: one token each.
  * A page that the kept tokens come to or lie on must belong to one sequence and
@@ -324,7 +325,9 @@ mi_decode_status_t mi_decode_rms_norm_f8(mi_decode_handle_t h, mi_decode_dtype_t
  *   xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]: binary32, rows
  *   ldxs and ldws apart.  bias [N] of type dtype, or NULL.  y: rows ldy >= N apart.
  * Any alignment to elements is taken; rows of x and w that begin and end at
- * multiples of 4 bytes are faster, and many rows at multiples of 16.  M == 0 or N == 0: nothing is done; K == 0: y = bias, or 0.
+ * multiples of 4 bytes are faster, and many rows at multiples of 16.  Others
+ * have at most 64 * 65535 tokens a call (ERR_UNSUPPORTED from there on).
+ * M == 0 or N == 0: nothing is done; K == 0: y = bias, or 0.
  * y must not overlap any input.
  */
 mi_decode_status_t mi_decode_f8_linear(mi_decode_handle_t h, mi_decode_dtype_t dtype, int64_t M,

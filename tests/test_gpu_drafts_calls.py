@@ -1,0 +1,242 @@
+"""Calls of the operators for drafted tokens: streams, devices, odd strides, the runtime's errors, launch limits, graphs."""
+import ctypes
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+decode = pytest.importorskip("dense_fp16_gemm_hgemm_amd.decode")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+from test_gpu_decode_attend import make, put  # noqa: E402
+
+DEV = torch.device("cuda", 0)
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def d():
+    h = decode.Decode()
+    yield h
+    h.close()
+
+
+def parts(seed, drafts=(5, 3), past=(300, 41)):
+    """A cache with context and drafts of two sequences, and everything that the calls take."""
+    lens = [p + n for p, n in zip(past, drafts)]
+    cache, table, cu, q = make(lens, list(drafts), 8, 2, 64, 16, torch.int8, torch.float16, seed)
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    rand = lambda *s: torch.randn(s, device=DEV, generator=gen).half()  # noqa: E731
+    T = sum(drafts)
+    seen, depth = zip(*(decode.tree([-1] + [i // 2 for i in range(n - 1)]) for n in drafts))
+    table = table.to(DEV)
+    return dict(most=max(drafts), cache=cache, table=table, cu=put([0, *torch.tensor(drafts).cumsum(0).tolist()]), q=q, lens=put(lens), past=put(list(past)),
+                seen=torch.cat(seen).to(DEV), positions=torch.cat([p + x for p, x in zip(past, depth)]).to(DEV, torch.int32),
+                kv=rand(T, 2, 64), rope=decode.rope_table(table.shape[1] * 16, 64), x=rand(T, 512), r=rand(T, 512), g=rand(512),
+                w=decode.f8_quantize(rand(256, 512)), keep=put([1, 4, 2]), cuk=put([0, 2, 3]), src=put([0, 3]), dst=put([2, 1]))
+
+
+def tensors(cache):
+    return [t.view(torch.uint8) for t in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+
+
+def calls(d, p, **kw):
+    """Each call's name and its result; those that write the cache come last and give its tensors."""
+    codes, scales, total = d.rms_norm_f8(p["x"], p["g"], p["r"], **kw)
+    yield "codes", codes.view(torch.uint8)
+    yield "scales", scales
+    yield "total", total
+    yield "f8_linear", d.f8_linear(codes, scales, p["w"].weight, p["w"].scales, **kw)
+    yield "kv_attend_tree", d.kv_attend_tree(p["q"], p["cache"], p["table"], p["lens"], p["seen"], p["cu"], **kw)
+    yield "kv_append", d.kv_append(p["cache"], p["kv"], p["kv"], p["table"], p["past"], p["cu"], q=p["q"], rope=p["rope"],
+                                   positions=p["positions"], **kw)
+    d.kv_keep(p["cache"], p["table"], p["past"], p["keep"], p["cuk"], **kw)
+    d.kv_copy(p["cache"], p["src"], p["dst"], **kw)
+
+
+def owner(x):
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= x.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_results_belong_to_the_stream_that_is_named(d):
+    """Each call with stream= and no out, behind work on that stream."""
+    p = parts(7)
+    before = [t.clone() for t in tensors(p["cache"])]
+    want = dict(calls(d, p))
+    held = [t.clone() for t in tensors(p["cache"])]
+    busy = torch.randn((2048, 2048), device=DEV)
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        for t, old in zip(tensors(p["cache"]), before):
+            t.copy_(old)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            busy @ busy
+        got = dict(calls(d, p, stream=handle))
+        for name, x in got.items():
+            assert owner(x) == side.cuda_stream, name
+            torch.full_like(x, 7)  # on the current stream: not the same memory
+        side.synchronize()
+        for name, x in got.items():
+            assert torch.equal(x, want[name]), name
+        for t, x in zip(tensors(p["cache"]), held):
+            assert torch.equal(t, x)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_a_handle_of_another_device_is_refused():
+    """Its kernels would run there."""
+    p = parts(11)
+    codes, scales = torch.zeros((2, 512), device=DEV).to(E4M3), torch.zeros((2, 4), device=DEV)
+    with decode.Decode() as other:
+        other.device += 1  # as a handle that was made there
+        for call in (lambda: other.rms_norm_f8(p["x"]),
+                     lambda: other.f8_linear(codes, scales, p["w"].weight, p["w"].scales),
+                     lambda: other.kv_attend_tree(p["q"], p["cache"], p["table"], p["lens"], p["seen"], p["cu"]),
+                     lambda: other.kv_append(p["cache"], p["kv"], p["kv"], p["table"], p["past"], p["cu"], q=p["q"], rope=p["rope"],
+                                             positions=p["positions"]),
+                     lambda: other.kv_keep(p["cache"], p["table"], p["past"], p["keep"], p["cuk"]),
+                     lambda: other.kv_copy(p["cache"], p["src"], p["dst"])):
+            with pytest.raises(ValueError, match="handle is on cuda"):
+                call()
+
+
+def test_tensors_of_another_device_are_refused(d):
+    p = parts(13)
+    codes, scales = torch.zeros((2, 512), device=DEV).to(E4M3), torch.zeros((2, 4), device=DEV)
+    w = p["w"]
+    for call in (lambda: d.rms_norm_f8(p["x"].cpu()), lambda: d.rms_norm_f8(p["x"], p["g"].cpu()),
+                 lambda: d.rms_norm_f8(p["x"], None, p["r"].cpu()),
+                 lambda: d.f8_linear(codes.cpu(), scales, *w), lambda: d.f8_linear(codes, scales.cpu(), *w),
+                 lambda: d.f8_linear(codes, scales, w.weight.cpu(), w.scales), lambda: d.f8_linear(codes, scales, w.weight, w.scales.cpu()),
+                 lambda: d.f8_linear(codes, scales, *w, bias=torch.zeros(256).half()),
+                 lambda: d.kv_attend_tree(p["q"], p["cache"], p["table"], p["lens"], p["seen"].cpu(), p["cu"]),
+                 lambda: d.kv_append(p["cache"], p["kv"], p["kv"], p["table"], p["past"], p["cu"], q=p["q"], rope=p["rope"],
+                                     positions=p["positions"].cpu()),
+                 lambda: d.kv_keep(p["cache"], p["table"], p["past"], p["keep"].cpu(), p["cuk"]),
+                 lambda: d.kv_copy(p["cache"], p["src"].cpu(), p["dst"]), lambda: d.kv_copy(p["cache"], p["src"], p["dst"].cpu())):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_strides_of_single_elements_do_not_matter(d):
+    """One token, one sequence and one page, cut from tensors of odd strides."""
+    p = parts(17, (1,), (50,))
+
+    def odd(x, *strides):
+        room = torch.zeros(x.numel() + 600, dtype=x.dtype, device=DEV)
+        return room.as_strided(x.shape, strides).copy_(x)
+
+    want = d.rms_norm_f8(p["x"], p["g"], p["r"])
+    got = d.rms_norm_f8(odd(p["x"], 3, 1), p["g"], odd(p["r"], 0, 1), total=odd(want[2], 1, 1))
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    y = d.f8_linear(want[0], want[1], *p["w"])
+    codes = torch.zeros(600, dtype=torch.uint8, device=DEV).as_strided((1, 512), (5, 1)).copy_(want[0].view(torch.uint8)).view(E4M3)
+    assert torch.equal(d.f8_linear(codes, odd(want[1], 1, 1), *p["w"]), y)
+    one = d.f8_linear(want[0], want[1], p["w"].weight[:1], p["w"].scales[:1])  # one weight row
+    assert torch.equal(d.f8_linear(want[0], want[1], p["w"].weight[:1], odd(p["w"].scales[:1], 2, 1)), one)
+    seen = odd(p["seen"], 9, 4)
+    o = d.kv_attend_tree(p["q"], p["cache"], p["table"], p["lens"], p["seen"])
+    assert torch.equal(d.kv_attend_tree(odd(p["q"], 7, 64, 1), p["cache"], odd(p["table"], 3, 1), odd(p["lens"], 4), seen), o)
+    before = [t.clone() for t in tensors(p["cache"])]
+    d.kv_keep(p["cache"], odd(p["table"], 3, 1), odd(p["past"], 5), odd(put([0]), 7))  # stays where it is
+    for t, old in zip(tensors(p["cache"]), before):
+        assert torch.equal(t, old)
+
+
+def test_an_earlier_error_of_the_runtime_is_not_a_calls_own(d):
+    with open("/proc/self/maps", encoding="utf-8") as f:
+        hip = ctypes.CDLL(next(line.split()[-1] for line in f if "libamdhip64" in line))
+    p = parts(19)
+    want = dict(calls(d, p))
+    p = parts(19)
+    torch.cuda.synchronize()
+    got = {}
+    try:
+        assert hip.hipSetDevice(99) != 0  # a refused call, which the runtime remembers
+        codes, scales, total = torch.empty((8, 512), device=DEV, dtype=E4M3), torch.empty((8, 4), device=DEV), torch.empty_like(p["x"])
+        hip.hipSetDevice(99)
+        d.rms_norm_f8(p["x"], p["g"], p["r"], codes=codes, scales=scales, total=total)
+        d.kv_keep(p["cache"], p["table"], p["past"], p["keep"], p["cuk"])
+        d.kv_copy(p["cache"], p["src"], p["dst"])
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    got = {"codes": codes.view(torch.uint8), "scales": scales, "total": total}
+    for name, x in got.items():
+        assert torch.equal(x, want[name]), name
+
+
+def test_more_rows_than_a_launch_can_have_are_unsupported(d):
+    """Threads of a launch are counted in 32 bits: four rows of up to 512 columns to 256 threads."""
+    x = torch.zeros((1 << 26, 1), device=DEV).half()
+    with pytest.raises(decode.DecodeError) as e:
+        d.rms_norm_f8(x)
+    assert e.value.status == decode.MI_DECODE_ERR_UNSUPPORTED
+    codes, scales, _ = d.rms_norm_f8(x[4:])
+    assert not scales.any() and not codes.view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("K", [8, 16, 24])
+def test_linear_layers_of_very_many_tokens(d, K):
+    """More than 64 * 65535, with few weight rows."""
+    M = 64 * 65535 + 70
+    x = torch.zeros((M, K), device=DEV).to(E4M3)
+    x.view(torch.uint8)[-1] = 0x38  # 1
+    scales = torch.ones((M, 1), device=DEV)
+    w = torch.ones((3, K), device=DEV).to(E4M3)
+    y = d.f8_linear(x, scales, w, scales[:1])
+    assert torch.all(y[-1] == K) and not y[:-1].any()
+    if K == 24:  # rows at odd bytes
+        with pytest.raises(decode.DecodeError) as e:
+            d.f8_linear(x[:, :23], scales, w[:, :23], scales[:1])
+        assert e.value.status == decode.MI_DECODE_ERR_UNSUPPORTED
+        y = d.f8_linear(x[70:, :23], scales[70:], w[:, :23], scales[:1])
+        assert torch.all(y[-1] == 23) and not y[:-1].any()
+
+
+def test_two_handles_on_two_streams_at_once(d):
+    """Split attention of two sets of drafts, each with a workspace of its own, side by side."""
+    sets = [parts(23, (12, 9), (9000, 4000)), parts(29, (12, 9), (7000, 6000))]
+    run = lambda h, p: h.kv_attend_tree(p["q"], p["cache"], p["table"], p["lens"], p["seen"], p["cu"])  # noqa: E731
+    want = [run(d, p) for p in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with decode.Decode() as other:
+        got = []
+        for _ in range(20):
+            for h, p, s in zip((d, other), sets, streams):
+                with torch.cuda.stream(s):
+                    got.append(run(h, p))
+        torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 2]), i
+
+
+def test_two_graphs_of_one_handle_in_turn(d):
+    """They share the workspace: replayed one after the other, with eager calls between."""
+    sets = [parts(31, (12, 9), (9000, 4000)), parts(37, (40, 33), (7000, 6000))]
+
+    def run(p):
+        codes, scales, total = d.rms_norm_f8(p["x"], p["g"], p["r"])
+        return (d.kv_attend_tree(p["q"], p["cache"], p["table"], p["lens"], p["seen"], p["cu"], p["most"]),
+                d.f8_linear(codes, scales, *p["w"]), total)
+
+    want = [run(p) for p in sets]
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for p in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(p))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        again = run(sets[0])
+        torch.cuda.synchronize()
+        for a, b in zip((*outs[0], *outs[1], *again), (*want[0], *want[1], *want[0])):
+            assert torch.equal(a, b)
