@@ -87,61 +87,45 @@ __device__ inline void store4(const F8Args& p, int m, int n, f32x4 y, bool whole
 
 // ------------------------------------------------------- rows at any byte --
 
-// For rows that do not begin at multiples of 4 bytes, or lie very far apart: MT x
-// NT tiles of 16 tokens by 16 weight rows to a workgroup, whose waves split K and
-// load operands from memory: wave w of W takes blocks w, w + W, ..., U in flight.
-template <bool BF16, int MT, int NT, int U>
+// A piece of 16 bytes from column k on, which was read 16 columns before K where it
+// crosses K, without the bytes that lie past K.
+__device__ inline u32x4 trim_bytes(u32x4 w, int k, int K) {
+  const int by = min(max(k + 16 - K, 0), 16), bits = 8 * (by & 7);
+  uint64_t lo = w[0] | (uint64_t)w[1] << 32, hi = w[2] | (uint64_t)w[3] << 32;
+  if (by & 8) lo = hi, hi = 0;
+  lo = bits ? lo >> bits | hi << (64 - bits) : lo;
+  hi >>= bits;
+  if (by == 16) lo = hi = 0;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// For few tokens and weight rows that do not begin at multiples of 4 bytes, or lie
+// very far apart: 16 tokens by 16 weight rows to a workgroup, whose waves split K
+// and load operands from memory: wave w of W takes blocks w, w + W, ..., U in flight.
+template <bool BF16>
 __global__ __launch_bounds__(1024) void f8_any_kernel(F8Args p, int whole) {
+  constexpr int U = 2;
   extern __shared__ __attribute__((aligned(16))) float red[];
   const int lane = threadIdx.x & 63, W = (int)(blockDim.x >> 6);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4, KB = (p.K + 127) >> 7;
-  const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
-  const uint8_t* wp[NT];
-  const uint8_t* xp[MT];
-  const float* sp[MT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) wp[t] = p.w + (int64_t)min(n0 + 16 * t + r, p.N - 1) * p.ldw;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t row = min(m0 + 16 * t + r, p.M - 1);
-    xp[t] = p.x + row * p.ldx;
-    sp[t] = p.xs + row * p.ldxs;
-  }
-  u32x4 wq[U][NT][2], xq[U][MT][2];
-  float xs[U][MT], ws[U][NT];
+  const int n0 = blockIdx.x * 16;
+  const uint8_t* wp = p.w + (int64_t)min(n0 + r, p.N - 1) * p.ldw;
+  const uint8_t* xp = p.x + (int64_t)min(r, p.M - 1) * p.ldx;
+  const float* sp = p.xs + (int64_t)min(r, p.M - 1) * p.ldxs;
+  u32x4 wq[U][2], xq[U][2];
+  float xs[U], ws[U];
   auto load = [&](int u, int kb) {
     const int at = min(kb, KB - 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      // a piece that crosses K is read 16 columns before K and shifted
       const int k = min(128 * at + 32 * g + 16 * i, p.K - 16);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) wq[u][t][i] = *reinterpret_cast<const loose*>(wp[t] + k);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) xq[u][t][i] = *reinterpret_cast<const loose*>(xp[t] + k);
+      wq[u][i] = *reinterpret_cast<const loose*>(wp + k);
+      xq[u][i] = *reinterpret_cast<const loose*>(xp + k);
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) ws[u][t] = p.ws[min(n0 + 16 * t, p.N - 1) / 128 * p.ldws + at];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) xs[u][t] = sp[t][at];
+    ws[u] = p.ws[n0 / 128 * p.ldws + at], xs[u] = sp[at];
   };
-  // without the bytes that lie past K
-  auto trim = [&](u32x4 w, int k) {
-    const int by = min(max(k + 16 - p.K, 0), 16), bits = 8 * (by & 7);
-    uint64_t lo = w[0] | (uint64_t)w[1] << 32, hi = w[2] | (uint64_t)w[3] << 32;
-    if (by & 8) lo = hi, hi = 0;
-    lo = bits ? lo >> bits | hi << (64 - bits) : lo;
-    hi >>= bits;
-    if (by == 16) lo = hi = 0;
-    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-  };
-  f32x4 total[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) total[m][t] = f32x4{0, 0, 0, 0};
-
+  f32x4 total = {0, 0, 0, 0};
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u, wave + u * W);
   for (int base = wave; base < KB; base += U * W) {
@@ -153,38 +137,21 @@ __global__ __launch_bounds__(1024) void f8_any_kernel(F8Args p, int whole) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int k = 128 * kb + 32 * g + 16 * i;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) wq[u][t][i] = trim(wq[u][t][i], k);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) xq[u][t][i] = trim(xq[u][t][i], k);
+          wq[u][i] = trim_bytes(wq[u][i], k, p.K), xq[u][i] = trim_bytes(xq[u][i], k, p.K);
         }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const f32x4 d = mma(wq[u][t][0], wq[u][t][1], xq[u][m][0], xq[u][m][1]);
-          const float s = xs[u][m] * ws[u][t];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) total[m][t][e] = __builtin_fmaf(d[e], s, total[m][t][e]);
-        }
+      add(total, mma(wq[u][0], wq[u][1], xq[u][0], xq[u][1]), xs[u] * ws[u]);
       load(u, base + (u + U) * W);
     }
   }
   // the waves' sums, added in their order
-  constexpr int PART = MT * NT * 64;
   f32x4* part = reinterpret_cast<f32x4*>(red);
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) part[wave * PART + (m * NT + t) * 64 + lane] = total[m][t];
+  part[threadIdx.x] = total;
   __syncthreads();
-  for (int i = threadIdx.x; i < PART; i += blockDim.x) {
-    f32x4 y = part[i];
-    for (int w = 1; w < W; ++w) y += part[w * PART + i];
-    const int l = i & 63, t = (i >> 6) % NT, m = (i >> 6) / NT;
-    store4<BF16>(p, m0 + 16 * m + (l & 15), n0 + 16 * t + 4 * (l >> 4), y, whole);
-  }
+  if (wave) return;
+  f32x4 y = part[lane];
+  for (int w = 1; w < W; ++w) y += part[64 * w + lane];
+  store4<BF16>(p, r, n0 + 4 * g, y, whole);
 }
 
 // K below 16, where no whole piece of a row exists: one result to a thread.
@@ -282,6 +249,101 @@ __device__ inline void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& t
   const int band = id / (GROUP * tiles_n), rows = min(GROUP, tiles_m - band * GROUP), in = id - band * GROUP * tiles_n;
   tm = band * GROUP + in % rows;
   tn = in / rows;
+}
+
+// For rows at any byte, or far apart: BM tokens by BN weight rows to a workgroup of
+// WM x WN waves.  Copies into shared memory need rows at multiples of 4 bytes, so a
+// block of 128 columns is loaded into registers while the one before is
+// multiplied, and stored from there, pieces exchanged as in f8_tile_kernel.
+//
+// Bound: latency, one block ahead (77 x 5003 x 4071 28 us, 26 with two; 512 x 4096 x
+// 4095 32 and 35; 4096^3 less one column 164, 840 TFLOP/s).  Each wave for itself with
+// operands from memory, as above, takes 69, 450 (345 with four strips of tokens) and 2700.
+template <bool BF16, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void f8_loose_kernel(F8Args p, int whole) {
+  constexpr int T = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16, PX = BM * 8 / T, PW = BN * 8 / T;
+  constexpr int XB = BM * 128, STAGE = XB + BN * 128 + BM * 4;
+  static_assert(PX * T == BM * 8 && PW * T == BN * 8 && BM <= T && 128 % BN == 0 && 2 * STAGE <= 160 << 10, "");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN, r = lane & 15, g = lane >> 4, KB = (p.K + 127) >> 7;
+  int tm, tn;
+  tile_of(blockIdx.x, (p.M + BM - 1) / BM, (p.N + BN - 1) / BN, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  // piece i of a thread: row (tid + T i) / 8, columns 16 c and on
+  const int c = tid & 7;
+  const uint8_t *xp[PX], *wp[PW];
+#pragma unroll
+  for (int i = 0; i < PX; ++i) xp[i] = p.x + (int64_t)min(m0 + (tid + T * i) / 8, p.M - 1) * p.ldx;
+#pragma unroll
+  for (int i = 0; i < PW; ++i) wp[i] = p.w + (int64_t)min(n0 + (tid + T * i) / 8, p.N - 1) * p.ldw;
+  const float* sp = p.xs + (int64_t)min(m0 + min(tid, BM - 1), p.M - 1) * p.ldxs;
+  const float* ws_row = p.ws + n0 / 128 * p.ldws;
+  u32x4 xq[PX], wq[PW];
+  float sq, ws;
+  auto load = [&](int kb) {
+    const int k = min(128 * kb + 16 * c, p.K - 16);
+#pragma unroll
+    for (int i = 0; i < PX; ++i) xq[i] = *reinterpret_cast<const loose*>(xp[i] + k);
+#pragma unroll
+    for (int i = 0; i < PW; ++i) wq[i] = *reinterpret_cast<const loose*>(wp[i] + k);
+    sq = sp[kb], ws = ws_row[kb];
+  };
+  auto store = [&](int kb) {
+    uint8_t* to = lds + (kb & 1) * STAGE;
+    const int k = 128 * kb + 16 * c;
+    if (128 * kb + 128 > p.K) {
+#pragma unroll
+      for (int i = 0; i < PX; ++i) xq[i] = trim_bytes(xq[i], k, p.K);
+#pragma unroll
+      for (int i = 0; i < PW; ++i) wq[i] = trim_bytes(wq[i], k, p.K);
+    }
+    auto at = [&](int i) {
+      const int row = (tid + T * i) / 8;
+      return 128 * row + 16 * (c ^ ((row >> 1) & 7));
+    };
+#pragma unroll
+    for (int i = 0; i < PX; ++i) *reinterpret_cast<u32x4*>(to + at(i)) = xq[i];
+#pragma unroll
+    for (int i = 0; i < PW; ++i) *reinterpret_cast<u32x4*>(to + XB + at(i)) = wq[i];
+    if (tid < BM) reinterpret_cast<float*>(to + XB + BN * 128)[tid] = sq * ws;
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
+  const int sw = (r >> 1) & 7, p0 = 128 * r + 16 * (g ^ sw), p1 = p0 ^ 64;
+  load(0);
+  for (int kb = 0; kb < KB; ++kb) {
+    store(kb);  // who still reads the block before does so in the other stage
+    __syncthreads();
+    if (kb + 1 < KB) load(kb + 1);
+    const uint8_t *x = lds + (kb & 1) * STAGE + wm * TM * 128, *w = lds + (kb & 1) * STAGE + XB + wn * TN * 128;
+    const float* sc = reinterpret_cast<const float*>(lds + (kb & 1) * STAGE + XB + BN * 128) + wm * TM + r;
+    u32x4 wf[FN][2], xf[FM][2];
+    float s[FM];
+#pragma unroll
+    for (int n = 0; n < FN; ++n) {
+      wf[n][0] = *reinterpret_cast<const u32x4*>(w + 2048 * n + p0);
+      wf[n][1] = *reinterpret_cast<const u32x4*>(w + 2048 * n + p1);
+    }
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      xf[m][0] = *reinterpret_cast<const u32x4*>(x + 2048 * m + p0);
+      xf[m][1] = *reinterpret_cast<const u32x4*>(x + 2048 * m + p1);
+      s[m] = sc[16 * m];
+    }
+    products<FM * FN>(
+        [&](int i) { return mma(wf[i % FN][0], wf[i % FN][1], xf[i / FN][0], xf[i / FN][1]); },
+        [&](int i, f32x4 d) -> f32x4& { return add(acc[i / FN][i % FN], d, s[i / FN]); },
+        [](int) {});
+  }
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      store4<BF16>(p, m0 + wm * TM + 16 * m + r, n0 + wn * TN + 16 * n + 4 * g, acc[m][n], whole);
 }
 
 // BM tokens by BN weight rows to a workgroup of WM x WN waves; a stage of the
@@ -653,16 +715,17 @@ __global__ __launch_bounds__(64 * W) void f8_strip_kernel(F8Args p, int whole) {
 
 // ----------------------------------------------------------------- choice --
 
-template <bool BF16, int MT, int NT, int U>
+template <bool BF16>
 hipError_t any(const F8Args& a, int whole, hipStream_t s) {
-  const int KB = (a.K + 127) / 128;
-  const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * MT - 1) / (16 * MT));
-  if (grid.y > 65535) return hipErrorInvalidConfiguration;
-  const int64_t each = ((int64_t)grid.x * grid.y + a.cus - 1) / a.cus;
-  int waves = each < 16 ? 16 / (int)each : 1;
-  if (waves < 4) waves = 4;
-  if (waves > KB) waves = KB;
-  return launch(f8_any_kernel<BF16, MT, NT, U>, grid, 64 * waves, waves * MT * NT * 1024, s, a, whole);
+  const int KB = (a.K + 127) / 128, waves = KB < 16 ? KB : 16;
+  return launch(f8_any_kernel<BF16>, dim3((a.N + 15) / 16), 64 * waves, waves * 1024, s, a, whole);
+}
+
+template <bool BF16, int BM, int BN, int WM, int WN>
+hipError_t loosely(const F8Args& a, int whole, hipStream_t s) {
+  const int64_t all = ((int64_t)a.M + BM - 1) / BM * (((int64_t)a.N + BN - 1) / BN);
+  if (all > INT32_MAX) return hipErrorInvalidConfiguration;
+  return launch(f8_loose_kernel<BF16, BM, BN, WM, WN>, dim3((unsigned)all), 64 * WM * WN, 0, s, a, whole);
 }
 
 template <bool BF16, int BM, int BN, int WM, int WN, int S>
@@ -700,16 +763,20 @@ hipError_t pick(const F8Args& a, hipStream_t s) {
     return a.K % n == 0 && a.ldx % n == 0 && a.ldw % n == 0 && reinterpret_cast<uintptr_t>(a.x) % n == 0 &&
            reinterpret_cast<uintptr_t>(a.w) % n == 0;
   };
+  const bool narrow = (a.N + 15) / 16 <= a.cus;
   if (!multiple(4) || a.ldx > 1 << 22 || a.ldw > 1 << 22 || a.ldxs > 1 << 20 || a.ldws > 1 << 20) {
-    if (a.M <= 16) return any<BF16, 1, 1, 2>(a, whole, s);
-    if (a.M <= 32) return any<BF16, 2, 1, 2>(a, whole, s);
-    return any<BF16, 4, 1, 1>(a, whole, s);
+    // us with strips and tiles: 1 token, K 4095, N 4096 18 and 23, N 14336 41 and 33;
+    // 16 tokens 32 and 28, 77 and 36; 8 tokens, N 500, K 11007 44 and 70.  Tiles of
+    // 64 and 128 rows: 512 tokens, K 4095, N 4096 32 and 45, N 14336 123 and 95; 4096
+    // tokens, N 4096 246 and 164.
+    if (a.M <= 16 && narrow) return any<BF16>(a, whole, s);
+    const int64_t small = ((int64_t)a.M + 63) / 64 * (((int64_t)a.N + 63) / 64);
+    return small <= 3 * a.cus ? loosely<BF16, 64, 64, 2, 2>(a, whole, s) : loosely<BF16, 128, 128, 2, 4>(a, whole, s);
   }
   // Up to 64 tokens: one strip of 16 weight rows to a compute unit while there are
   // no more, else wider strips (us with strips of 16 rows and wider ones, K 4096:
   // 1 token, N 4096 6.0 and 6.4, N 14336 17.3 and 15.3; 32 tokens, N 4096 6.9 and
   // 11.4, N 14336 24.5 and 18.5; 64 tokens, N 4096 9.8 and 15.3, N 14336 36 and 20.7).
-  const bool narrow = (a.N + 15) / 16 <= a.cus;
   if (a.M <= 16) return narrow ? strips<BF16, 1, 1, 2, 16>(a, whole, s) : strips<BF16, 1, 2, 2, 12>(a, whole, s);
   if (a.M <= 32) return narrow ? strips<BF16, 2, 1, 2, 12>(a, whole, s) : strips<BF16, 2, 4, 3, 4>(a, whole, s);
   if (a.M <= 64) return narrow ? strips<BF16, 4, 1, 2, 6>(a, whole, s) : strips<BF16, 4, 4, 2, 4>(a, whole, s);

@@ -325,8 +325,7 @@ mi_decode_status_t mi_decode_rms_norm_f8(mi_decode_handle_t h, mi_decode_dtype_t
  *   xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]: binary32, rows
  *   ldxs and ldws apart.  bias [N] of type dtype, or NULL.  y: rows ldy >= N apart.
  * Any alignment to elements is taken; rows of x and w that begin and end at
- * multiples of 4 bytes are faster, and many rows at multiples of 16.  Others
- * have at most 64 * 65535 tokens a call (ERR_UNSUPPORTED from there on).
+ * multiples of 4 bytes are faster, and many rows at multiples of 16.
  * M == 0 or N == 0: nothing is done; K == 0: y = bias, or 0.
  * y must not overlap any input.
  */

@@ -191,10 +191,7 @@ def test_linear_layers_of_very_many_tokens(d, K):
     y = d.f8_linear(x, scales, w, scales[:1])
     assert torch.all(y[-1] == K) and not y[:-1].any()
     if K == 24:  # rows at odd bytes
-        with pytest.raises(decode.DecodeError) as e:
-            d.f8_linear(x[:, :23], scales, w[:, :23], scales[:1])
-        assert e.value.status == decode.MI_DECODE_ERR_UNSUPPORTED
-        y = d.f8_linear(x[70:, :23], scales[70:], w[:, :23], scales[:1])
+        y = d.f8_linear(x[:, :23], scales, w[:, :23], scales[:1])
         assert torch.all(y[-1] == 23) and not y[:-1].any()
 
 

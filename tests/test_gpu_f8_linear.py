@@ -222,3 +222,18 @@ def test_refusals(d):
     with pytest.raises(decode.DecodeError):  # the output over the scales
         both = torch.zeros(4000, device=DEV)
         d.f8_linear(x, both[:8].view(4, 2), w, ws, out=both.view(torch.float16)[:800].view(4, 200))
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 5000, 129), (16, 4100, 127), (17, 64, 255), (63, 65, 1153), (64, 64, 18), (65, 130, 131),
+                                     (1700, 2000, 143), (800, 5003, 515), (1025, 3100, 257)])
+def test_rows_at_odd_bytes(d, M, N, K):
+    """Products, places and rows apart, where nothing but single bytes is aligned."""
+    for dtype in (torch.float16, torch.bfloat16):
+        x, xs, w, ws, b = make(M, N, K, M + N + K, dtype)
+        y = d.f8_linear(x, xs, w, ws, bias=b, dtype=dtype)
+        check_linear(y, x, xs, w, ws, b)
+    room = [torch.full((r, K + 6), 0x7f, dtype=torch.uint8, device=x.device) for r in (M, N)]  # NaN between the rows
+    for to, of in zip(room, (x, w)):
+        to[:, 3:3 + K] = of.view(torch.uint8)
+    cut = [r.view(x.dtype)[:, 3:3 + K] for r in room]
+    assert torch.equal(d.f8_linear(cut[0], xs, cut[1], ws, bias=b, dtype=dtype), y)
