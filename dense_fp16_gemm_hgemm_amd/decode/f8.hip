@@ -178,16 +178,18 @@ __device__ inline u32x4 raw_rsrc(const void* base, uint32_t bytes) {
 }
 __device__ inline uint32_t lds_at(const void* p) { return (uint32_t)reinterpret_cast<uint64_t>(p); }
 // A lane's 16 or 4 bytes at voff + soff go to shared memory at lds + PLUS + 16 or 4 times the lane.
+// A copy reads m0 one wait state after it is written at the earliest, which the
+// compiler sees to for its own copies and not within asm.
 template <int PLUS>
 __device__ __forceinline__ void copy16(const u32x4& rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %0, %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc), "s"(soff), "n"(PLUS)
                : "memory", "m0", "scc");
 }
 template <int PLUS>
 __device__ __forceinline__ void copy4(const u32x4& rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %0, %4\n\tbuffer_load_dword %1, %2, %3 offen lds"
+  asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc), "s"(soff), "n"(PLUS)
                : "memory", "m0", "scc");
