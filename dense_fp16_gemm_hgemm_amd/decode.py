@@ -56,7 +56,7 @@ from typing import NamedTuple, Optional
 import torch  # imported first so that both use one HIP runtime
 
 __all__ = ["Decode", "DecodeError", "KvCache", "W4", "w4_pack", "w4_unpack", "w4_quantize",
-           "F8", "f8_quantize", "f8_values", "tree", "rope_table", "LIB_PATH"]
+           "F8", "f8_quantize", "f8_values", "tree", "tree_window", "rope_table", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmi_decode.so")
 if not os.path.exists(LIB_PATH):
@@ -312,6 +312,32 @@ def tree(parents):
     return torch.where(seen >= 2 ** 31, seen - 2 ** 32, seen).to(torch.int32), torch.tensor(depth, dtype=torch.int32)
 
 
+def tree_window(seen, depth, cu, past, window, sinks=0):
+    """``seen`` without the drafted tokens that a window hides, so that ``Decode.kv_attend_tree`` with this
+    window sees of a branch what ``Decode.kv_attend`` sees of a sequence: the last `window` tokens up to a
+    token's own position, and those at positions below `sinks`.  Trees of at most `window` levels stay as
+    they are.
+
+    ``seen`` int32 [tokens, words] and ``depth`` int32 [tokens] are what ``tree`` gives, sequence b's rows
+    from cu[b] on; ``past``: the tokens before each sequence's drafts.  Where the tensors are; captured
+    calls read them when they are replayed."""
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    T, words = seen.shape
+    if window == 0 or T == 0 or words == 0:
+        return seen
+    at, bit = torch.arange(T, device=seen.device), torch.arange(32 * words, device=seen.device)
+    seq = torch.searchsorted(cu[1:], at.to(cu.dtype), right=True).clamp(max=past.shape[0] - 1)
+    other = depth[(cu[seq].long()[:, None] + bit).clamp(0, T - 1)].long()  # the depth of each bit's token
+    hidden = other <= depth.long()[:, None] - window
+    if sinks:
+        hidden &= past[seq].long()[:, None] + other >= sinks
+    # A row whose ancestors are hidden still stands behind the context by as many tokens as the window
+    # has besides itself, which hides the whole context as its true position does.
+    mask = (hidden.view(T, words, 32).long() << bit[:32]).sum(-1)
+    return seen & ~torch.where(mask >= 2 ** 31, mask - 2 ** 32, mask).to(torch.int32)
+
+
 def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """float32 [positions, rot_dim]: cosines, then sines, of position * base^(-2 i / rot_dim),
     with the angles in float64."""
@@ -450,7 +476,8 @@ class Decode:
         its sequence's drafted token a (``tree`` makes them).  Of the tokens before the drafts it
         sees all, or those of a window: the last `window` ones up to its own position, which is
         behind them by the number of drafted tokens that it sees besides itself, and the first
-        `sinks`."""
+        `sinks`.  Of the drafted tokens the bits alone say what it sees: of a tree with more levels
+        than the window has tokens, ``tree_window`` takes out those that the window hides."""
         return _done(_calls.kv_attend_tree(self.handle, self.device, cache._at, cache._dev, q, table, lens, cu_q, max_q,
                                            max_len, window, sinks, scale, out,
                                            stream if stream is None else _raw(stream, cache.device), seen),

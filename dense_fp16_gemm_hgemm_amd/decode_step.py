@@ -22,7 +22,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import Hgemm
-from .decode import F8, W4, Decode, KvCache, f8_quantize, rope_table, tree, w4_quantize, w4_unpack
+from .decode import F8, W4, Decode, KvCache, f8_quantize, rope_table, tree, tree_window, w4_quantize, w4_unpack
 
 
 class Config(NamedTuple):
@@ -130,6 +130,8 @@ class Model:
         room = self.cols * c.page_size
         if self.longest + most > room:
             raise ValueError(f"the page table has room for {room} tokens a sequence, not for {self.longest + most}")
+        if 0 < c.window < most:  # a branch may reach further back than the window
+            seen = tree_window(seen, depth, cu, self.lens, c.window, c.sinks)
         total = self.lens + drafts
         positions = depth + torch.repeat_interleave(self.lens, drafts, output_size=x.shape[0])
         more = None  # what the layer before adds to x

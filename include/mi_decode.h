@@ -242,7 +242,11 @@ mi_decode_status_t mi_decode_kv_append_at(mi_decode_handle_t h, const mi_decode_
  *   - context position j < c where window == 0, or j > p - window, or j < sinks,
  *     with p = c + the number of drafted tokens other than itself that it sees
  *     (for a tree, the position of its depth);
- *   - drafted tokens by their bits alone, whatever the window is.
+ *   - drafted tokens by their bits alone, whatever the window is.  So a row of
+ *     a tree with more levels than the window has tokens must not have the bits
+ *     of ancestors at positions <= its own - window (and >= sinks), if it is to
+ *     see what mi_decode_kv_attend would show it; p is then below its position
+ *     and hides the same of the context, all but the sinks.
  * seen_words * 32 must be at least batch->max_tokens, and seen_stride at least
  * seen_words.  A query that sees nothing gives zeros.  Everything else is as in
  * mi_decode_kv_attend.
