@@ -295,7 +295,13 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n_args, bool tree) {
     if (hq < 1 || hq % c.kv_heads) refuse(PyExc_ValueError, "q must have a multiple of %d heads, got %lld", c.kv_heads, (long long)hq);
     const int32_t window = number32(a[10], "window"), sinks = number32(a[11], "sinks");
     if (window < 0 || sinks < 0) refuse(PyExc_ValueError, "window and sinks must not be negative");
-    const mi_decode_batch_t t = batch_of(a[5], a[6], a[7], T, longest(a[8], a[7], T, "max_q"), device, "lens", "cu_q");
+    const at::Tensor* seen = tree ? tensor(a[15], "seen") : nullptr;
+    const int32_t* bits = tree ? int32s(*seen, "seen", 2) : nullptr;
+    const int64_t words = tree ? seen->size(1) : 0;
+    int32_t most = longest(a[8], a[7], T, "max_q");
+    // a row of bits has one for each drafted token of its sequence
+    if (tree && a[8] == Py_None) most = (int32_t)std::min<int64_t>(most, std::max<int64_t>(32 * words, 1));
+    const mi_decode_batch_t t = batch_of(a[5], a[6], a[7], T, most, device, "lens", "cu_q");
     const int64_t max_len = a[9] == Py_None ? (int64_t)t.table_cols * c.page_size : number(a[9]);
     const double scale = a[12] == Py_None ? 1.0 / std::sqrt((double)c.head_dim) : PyFloat_AsDouble(a[12]);
     if (PyErr_Occurred()) throw Refused{};
@@ -313,15 +319,12 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n_args, bool tree) {
     if (!tree)
       return result(mi_decode_kv_attend(handle(a[0]), &c, type, &t, max_len, (int32_t)hq, &rq, &ro, (float)scale, window, sinks,
                                         stream.raw), *out);
-    const at::Tensor& seen = *tensor(a[15], "seen");
-    const int32_t* bits = int32s(seen, "seen", 2);
-    const int64_t words = seen.size(1);
-    if (seen.size(0) != T) refuse(PyExc_ValueError, "seen must have one row a token (%lld), got %lld", (long long)T, (long long)seen.size(0));
+    if (seen->size(0) != T) refuse(PyExc_ValueError, "seen must have one row a token (%lld), got %lld", (long long)T, (long long)seen->size(0));
     if (words > INT32_MAX || (T > 0 && words * 32 < t.max_tokens))
       refuse(PyExc_ValueError, "seen has %lld words of 32 bits a token, too few for max_q=%d", (long long)words, t.max_tokens);
-    on(&seen, device, "seen");
+    on(seen, device, "seen");
     return result(mi_decode_kv_attend_tree(handle(a[0]), &c, type, &t, max_len, (int32_t)hq, &rq, &ro, bits,
-                                           T > 1 ? seen.stride(0) : words, (int32_t)words, (float)scale, window, sinks,
+                                           T > 1 ? seen->stride(0) : words, (int32_t)words, (float)scale, window, sinks,
                                            stream.raw), *out);
   });
 }

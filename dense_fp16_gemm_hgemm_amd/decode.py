@@ -477,7 +477,9 @@ class Decode:
         sees all, or those of a window: the last `window` ones up to its own position, which is
         behind them by the number of drafted tokens that it sees besides itself, and the first
         `sinks`.  Of the drafted tokens the bits alone say what it sees: of a tree with more levels
-        than the window has tokens, ``tree_window`` takes out those that the window hides."""
+        than the window has tokens, ``tree_window`` takes out those that the window hides.
+        max_q: the most drafted tokens that a sequence has (rows of further ones are not written);
+        left out, as many as a row of `seen` has bits, or all of the call's."""
         return _done(_calls.kv_attend_tree(self.handle, self.device, cache._at, cache._dev, q, table, lens, cu_q, max_q,
                                            max_len, window, sinks, scale, out,
                                            stream if stream is None else _raw(stream, cache.device), seen),
