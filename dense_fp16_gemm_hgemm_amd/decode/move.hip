@@ -45,13 +45,21 @@ __device__ inline uint64_t abs_bits(double x) { return __builtin_bit_cast(uint64
 // Sixteen codes times ratio, to the nearest codes.  Scales of two pages are often
 // in a simple ratio, as the largest code sets the new one, and their products lie
 // on the border between two codes then: in binary64 the rounding to binary32
-// that follows takes the ratio's error away, and the border goes to even.
+// that follows takes the ratio's error away, and the border goes to even.  A NaN
+// stays one (to_code's bounds would make a number of it).
 template <int CODE>
 __device__ inline u32x4 rescaled(u32x4 w, double ratio) {
   u32x4 o = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < 16; ++e)
     o[e / 4] |= (uint32_t)to_code<CODE>((float)(from_code<CODE>((uint8_t)(w[e / 4] >> (8 * (e % 4)))) * ratio)) << (8 * (e % 4));
+  if constexpr (CODE == MI_DECODE_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t nan = (((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+      o[i] |= nan * 0x7fu;
+    }
+  }
   return o;
 }
 
