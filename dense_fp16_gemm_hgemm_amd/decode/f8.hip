@@ -259,7 +259,8 @@ __device__ inline void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& t
 // multiplied, and stored from there, pieces exchanged as in f8_tile_kernel.
 //
 // Bound: latency, one block ahead (77 x 5003 x 4071 28 us, 26 with two; 512 x 4096 x
-// 4095 32 and 35; 4096^3 less one column 164, 840 TFLOP/s).  Each wave for itself with
+// 4095 32 and 35; 4096^3 less one column 160, 860 TFLOP/s, matrix pipes busy in 21 % of
+// the cycles).  Each wave for itself with
 // operands from memory, as above, takes 69, 450 (345 with four strips of tokens) and 2700.
 template <bool BF16, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void f8_loose_kernel(F8Args p, int whole) {
@@ -353,7 +354,10 @@ __global__ __launch_bounds__(64 * WM * WN) void f8_loose_kernel(F8Args p, int wh
 // exchanged by (row / 2) % 8, so that eight rows' reads of one piece meet no bank
 // twice.
 //
-// Bound: copies, reads and products side by side, none of them alone.  1024 x 4096
+// Bound: copies, reads and products side by side, none of them alone; the smaller the
+// tile, the more copies to a product (matrix pipes busy in 13 % of the cycles at 77 x
+// 5003 x 4072 with 64 x 64, 22 at 512 x 4096 x 4096 with 64 x 128, 35 at 1024 with 128 x
+// 128, 47 at 2048 with 128 x 256).  1024 x 4096
 // x 4096 took 41 us with a stage's copies issued together and 28 with them spread
 // between its products; on the way, at 32, leaving out the copies, the reads or the
 // products (a copy, for timing) left 22, 24 and 26.  Two, three or four stages
@@ -489,9 +493,10 @@ __global__ __launch_bounds__(64 * WM * WN) void f8_tile_kernel(F8Args p, int who
 // phase 2 kb + 2.  Each waits for its copies at the end of its next
 // multiplication, before the barrier behind which they are first read.
 //
-// Bound: matrix instructions.  8192 x 4096 x 11008 310 to 316 us, 2340 to 2380 TFLOP/s,
-// where a large library product with one scale for each operand reaches 2590; a
-// scaled addition is four vector instructions to 32 cycles of the matrix pipe.
+// Bound: matrix instructions.  8192 x 4096 x 11008 310 to 323 us on different boards,
+// 2290 to 2380 TFLOP/s, where a large library product with one scale for each operand
+// reaches 2590; matrix pipes are busy in 64 % of the cycles.  A scaled addition is four
+// vector instructions to 32 cycles of the matrix pipe.
 template <bool BF16, int BN>
 __global__ __launch_bounds__(512) void f8_turns_kernel(F8Args p, int whole) {
   constexpr int BM = 256, TN = BN / 4, FM = 8, FN = TN / 16, XB = BM * 128, WB = BN * 128, STAGE = XB + WB + 4 * BM + 256;
@@ -598,9 +603,12 @@ __global__ __launch_bounds__(512) void f8_turns_kernel(F8Args p, int whole) {
 // shared memory, so that no wave waits for another before the sums are added.
 //
 // Bound: launch and one or two rounds of loads for small weights (1 x 4096 x 4096
-// 6.0 us with weights from memory, 4.9 from the last-level cache), the weights' bytes
-// for large ones (1 x 14336 x 4096 15.3, 3.8 TB/s).  With operands in registers
-// instead, which hold fewer loads in flight, 64 x 4096 x 4096 took 22 us; here 9.8.
+// 5.7 us with weights from memory, 4.8 from the last-level cache), the weights' bytes
+// for large ones (1 x 14336 x 4096 14.9, 3.9 TB/s).  With operands in registers
+// instead, which hold fewer loads in flight, 64 x 4096 x 4096 took 22 us; here 9.3.
+// Towards 64 tokens, copies of x: each wave copies all tokens' columns of its own
+// blocks, and each workgroup does so again, four fifths of the copied bytes with
+// strips of 16 rows and half with 64 (matrix pipes busy in 5 and 11 % of the cycles).
 template <bool BF16, int MT, int NT, int S, int W>
 __global__ __launch_bounds__(64 * W) void f8_strip_kernel(F8Args p, int whole) {
   constexpr int SCALES = (MT + 3) / 4, STAGE = 2048 * (MT + NT) + 256 * SCALES, COPIES = 2 * (MT + NT) + SCALES;

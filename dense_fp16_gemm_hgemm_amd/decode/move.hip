@@ -11,9 +11,9 @@ constexpr int kPiece = 16384;  // bytes of a page that a workgroup copies
 // A workgroup copies 16 KiB of a page's keys or values, a thread's four loads
 // in flight at once; the page's first one takes its scales along.
 //
-// Bound: bytes.  2048 pages of 8 heads x 16 tokens x 128 channels are 105 us, 5.1 TB/s
-// of reads and writes (a large copy reaches 4.9); one page is 3.6 us, an empty
-// kernel 3.3.
+// Bound: bytes.  2048 pages of 8 heads x 64 tokens x 128 channels are 105 us, 5.1 TB/s
+// of 537 MB of reads and writes (torch's copy of 2 GiB reaches 4.9); one page is
+// 3.6 us, an empty kernel 3.3.
 __global__ __launch_bounds__(256) void copy_kernel(CopyArgs p, int pieces) {
   const int64_t pair = blockIdx.x / (2 * pieces);
   const int rest = blockIdx.x % (2 * pieces), at = rest >> 1, is_v = rest & 1, H = p.cache.kv_heads;
@@ -87,9 +87,15 @@ __device__ inline void all_read() {
 // order of positions: a token comes from its own place or a later one, so what a
 // page reads no earlier page has written.
 //
-// Bound: those latencies, 4 us for one sequence and, 128 sequences with paths of a
-// dozen tokens over pages of 16, 9.7 us in eight rounds of workgroups (page by page,
-// with its loads for each page in turn, 14.6).
+// Bound: those latencies, 4 us for one sequence and, 128 sequences of 8 heads with
+// paths of a dozen tokens over pages of 16, 9.7 us (page by page, with its loads for
+// each page in turn, 14.6).  Their 2048 workgroups are resident all at once (up to 64
+// registers), their bytes are few, and vector instructions (binary64) issue in 42 % of
+// the cycles.  In a trace of fresh caches 1, 16, 64 and 128
+// sequences take 5.9, 6.8, 8.5 and 13.4 us; the 128 take 10.8 where no scale grows, and
+// 12.1 where the path begins a page, so that no older rows of it are read, rescaled
+// and stored behind the barrier.  Page by page 200 tokens take 23 us over pages of 64
+// and 56 over pages of 16.
 template <int CODE>
 __global__ __launch_bounds__(256) void keep_kernel(KeepArgs p) {
   constexpr int KEEP = 2, PAGES = KEEP * 64 / 16 + 1;  // pages of 16 that KEEP rows a thread of 64 channels lie on

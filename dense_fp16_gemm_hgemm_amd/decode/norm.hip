@@ -6,10 +6,14 @@
 // (sixteen threads hold 128 columns).  y is not rounded before it is divided by the
 // scale.  Above 16384 columns t is read again, from the caches for the most part.
 //
-// Bound: for many rows the bytes, x, r, t and codes at a large copy's rate (8192 x
-// 4096 bf16 57 us as nodes of a graph, 4.1 TB/s of 235 MB; the same read again
-// instead of kept 62, a wave to a row 69).  For few rows launch, one round of
-// loads, the exchanges and the division (1 x 4096 4.2 us, an empty kernel 3.3).
+// Bound: for many rows the bytes, x, r, t and codes (8192 x 4096 bf16, 235 MB: 48.4 us
+// in a trace, 4.9 TB/s, and 52 as nodes of a graph; the same read again instead of
+// kept 58, a wave to a row 67), and beside them vector instructions, the division of
+// each y by its scale among them, which issue in all of its cycles.  For few rows launch, one round of loads, the
+// exchanges and the division (1 x 4096 3.7 us, an empty kernel 3.3).  Rows that do not
+// begin at multiples of 16 bytes, or do not end at one of 8 columns, take eight loads
+// of 2 bytes and eight byte stores a thread, whose number is the bound then: 1, 512
+// and 8192 x 4095 6.6, 12.2 and 149 us where 4096 columns take 3.7, 6.6 and 52.
 #include "device.hpp"
 
 namespace mid {
@@ -195,10 +199,11 @@ hipError_t run(const NormArgs& a, hipStream_t s) {
 
 // Up to 512 rows take many threads with one or two groups of columns each, as
 // the time is one thread's chain; more rows take fewer threads, so that several
-// rows share a compute unit (us for 1, 512 and 8192 rows of 4096 columns: 512 threads
-// 4.2, 7.1, 61; 256 threads 5.1, 7.8, 57.  1 and 512 rows of 8192: 1024 threads 4.9,
-// 10.7; 256 threads 7.8, 12.4.  Of 16384: 1024 threads 7.0, 17.2; 512 threads 8.5, 18.5.
-// 512 rows of 1024: 256 threads 4.6, 64 threads 5.5).
+// rows share a compute unit.  us as nodes of a graph, more threads and fewer: 1, 512
+// and 8192 rows of 1024 columns 3.5, 4.1, 21.3 (256 threads) and 4.5, 5.1, 19.7 (64);
+// of 4096 3.7, 6.6, 55.6 (512) and 4.7, 7.3, 52.5 (256); 1, 512 and 4096 rows of 8192
+// 4.4, 10.3, 56.5 (1024) and 7.4, 11.8, 56.5 (256); 1, 512 and 2048 rows of 16384 6.6,
+// 18.5, 53.4 (1024) and 8.1, 19.5, 56.6 (512).
 template <bool BF16, bool WIDE>
 hipError_t pick(const NormArgs& a, hipStream_t s) {
   const bool few = a.M <= 512;
