@@ -9,11 +9,12 @@
 // Bound: for many rows the bytes, x, r, t and codes (8192 x 4096 bf16, 235 MB: 48.4 us
 // in a trace, 4.9 TB/s, and 52 as nodes of a graph; the same read again instead of
 // kept 58, a wave to a row 67), and beside them vector instructions, the division of
-// each y by its scale among them, which issue in all of its cycles.  For few rows launch, one round of loads, the
-// exchanges and the division (1 x 4096 3.7 us, an empty kernel 3.3).  Rows that do not
-// begin at multiples of 16 bytes, or do not end at one of 8 columns, take eight loads
-// of 2 bytes and eight byte stores a thread, whose number is the bound then: 1, 512
-// and 8192 x 4095 6.6, 12.2 and 149 us where 4096 columns take 3.7, 6.6 and 52.
+// each y by its scale among them, which issue in all of its cycles.  For few rows
+// launch, one round of loads, the exchanges and the division (1 x 4096 3.7 us, an empty
+// kernel 3.3).  Rows that do not begin at multiples of 16 bytes, or do not end at one
+// of 8 columns, take eight loads of 2 bytes and eight byte stores a thread, whose
+// number is the bound then: 1, 512 and 8192 x 4095 6.6, 12.2 and 149 us where 4096
+// columns take 3.7, 6.6 and 52.
 #include "device.hpp"
 
 namespace mid {

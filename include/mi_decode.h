@@ -269,10 +269,13 @@ mi_decode_status_t mi_decode_kv_attend_tree(mi_decode_handle_t h, const mi_decod
  * may be there more than once.
  * Scales.  For each page and head that positions lens[b] .. lens[b] + n - 1 lie
  * on: s' = max(s, max |x| / QMAX) over the tokens x that come from other pages.
- * Codes become round(code * (s_source / s')), 0 where s' is 0, with s' and the
- * ratio in binary64: those that come, and, where s' > s, those of all positions
- * up to lens[b] + n - 1 that the page holds.  So a token that stays on its page
- * keeps its code unless the scale grows.  A token from another page with a NaN
+ * Codes become round(code * (s_source / s')), 0 where s' is 0: those that come,
+ * and, where s' > s, those of all positions up to lens[b] + n - 1 that the page
+ * holds.  s', the ratio and the product are binary64, and the product is rounded
+ * to binary32 before the code's own rounding to nearest even, so that products
+ * on the border between two codes, which simple ratios have, are not moved off
+ * it by the ratio's error.  So a token that stays on its page keeps its code
+ * unless the scale grows, and a NaN code then stays one.  A token from another page with a NaN
  * code or a scale that is not finite leaves a scale that is not finite, as in
  * mi_decode_kv_append.
  * Positions from lens[b] + n on hold no token of the sequence afterwards.
