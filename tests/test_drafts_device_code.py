@@ -54,7 +54,7 @@ def listing(co):
             yield re.sub(r"\s+", " ", line.split("//")[0]).strip()
 
 
-def test_the_checker_finds_planted_mistakes():
+def test_planted_mistakes_are_found():
     copy = "buffer_load_dwordx4 v1, s[8:11], s14 offen lds"
     assert early_copies(["s_add_u32 m0, s1, s2", copy])[1]
     assert early_copies(["s_mov_b32 m0, s1", copy])[1]
